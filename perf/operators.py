@@ -157,7 +157,8 @@ def _values(q, s, dtype):
 
 def _quantize_plain(x):
     """d = amax / 127, code = x * (1 / d) rounded half away from zero; columns padded with zeros to 16."""
-    d = x.abs().amax(1) / 127.0
+    d = x.abs().amax(1)
+    d = d / torch.full_like(d, 127.0)          # a tensor: by a number, torch multiplies with its reciprocal
     inv = torch.where(d > 0, 1.0 / d, torch.zeros_like(d))
     inv = torch.where(torch.isinf(inv), torch.zeros_like(inv), inv)
     v = x * inv[:, None]
