@@ -24,6 +24,7 @@ EXPORTS = (
     "mmq_gemm_q4_K", "mmq_gemm_q5_K", "mmq_gemm_q6_K", "mmq_gemm_multi", "mmq_gemm_workspace_bytes",
     "mmq_gemm_multi_ws", "mmq_moe_workspace_bytes",
     "mmq_moe_gemm", "mmq_moe_gemm_routed", "mmq_moe_gemm_noalloc", "mmq_debug_block_dots",
+    "mmq_quantize_i8", "mmq_silu_mul_quantize_i8", "mmq_gemm_i8", "mmq_grouped_gemm_i8", "mmq_plan_i8",
     "mmq_last_error", "mmq_plan_describe", "mmq_plan_for_limits",
     "mmq_debug_set_extra_lds", "mmq_version",
 )
@@ -69,6 +70,16 @@ def lib() -> ctypes.CDLL:
         L.mmq_moe_gemm_routed.restype = i32
         L.mmq_moe_gemm_noalloc.argtypes = [i32, p, p, i32, p, i32, p, i64, i64, i64, p]
         L.mmq_moe_gemm_noalloc.restype = i32
+        L.mmq_quantize_i8.argtypes = [i32, p, i64, p, i64, p, i64, i64, p]
+        L.mmq_quantize_i8.restype = i32
+        L.mmq_silu_mul_quantize_i8.argtypes = [i32, p, p, i64, p, i64, p, i64, i64, p]
+        L.mmq_silu_mul_quantize_i8.restype = i32
+        L.mmq_gemm_i8.argtypes = [i32, p, i64, p, p, i64, p, p, p, i64, i64, i64, i64, p]
+        L.mmq_gemm_i8.restype = i32
+        L.mmq_grouped_gemm_i8.argtypes = [i32, p, i64, p, i64, p, p, i32, p, i64, p, p, i64, i64, i64, i64, p]
+        L.mmq_grouped_gemm_i8.restype = i32
+        L.mmq_plan_i8.argtypes = [i64, i64, i64, i32, i32, ctypes.c_char_p, i64]
+        L.mmq_plan_i8.restype = i32
         L.mmq_debug_block_dots.argtypes = [i32, p, p, p, i64, i64, i64, p]
         L.mmq_debug_block_dots.restype = i32
         L.mmq_last_error.argtypes = []
@@ -345,6 +356,190 @@ def debug_block_dots(fmt, xq, w, M, N, K, dots=None, stream=None):
     _check(lib().mmq_debug_block_dots(fmt, _ptr(xq), _ptr(w), _ptr(dots, torch.int32), M, N, K,
                                       _stream(stream)), "mmq_debug_block_dots")
     return dots
+
+
+# ---------------------------------------------------------------------------
+# Per-token / per-channel int8: codes int8 [rows, K] with one fp32 scale per
+# row; products of them in fp32, bf16 or fp16.  These calls take their sizes
+# from the tensors, accept rows with a pitch (a slice of columns) wherever
+# the library does, and run on the GPU that holds the tensors, whichever
+# device is current: on `stream`, or else on that GPU's current stream.
+# ---------------------------------------------------------------------------
+I8_MAX_K = 131056
+
+
+def _pad16(K) -> int:
+    return (K + 15) // 16 * 16
+
+
+def _type_code(dtype) -> int:
+    import torch
+    code = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}.get(dtype)
+    if code is None:
+        raise ValueError(f"expected torch.float32, torch.bfloat16 or torch.float16, got {dtype}")
+    return code
+
+
+def _matrix(t, what, dtype=None, rows=None, cols=None, dev=None):
+    """Row pitch of the matrix ``t`` in elements; its columns must be adjacent."""
+    if t.dim() != 2:
+        raise ValueError(f"{what}: expected a matrix, got shape {tuple(t.shape)}")
+    if dtype is not None and t.dtype != dtype:
+        raise ValueError(f"{what}: expected {dtype}, got {t.dtype}")
+    r, c = t.shape
+    if (rows is not None and r != rows) or (cols is not None and c != cols):
+        raise ValueError(f"{what}: expected shape ({rows if rows is not None else r}, "
+                         f"{cols if cols is not None else c}), got {tuple(t.shape)}")
+    _on(t, what, dev)
+    sr, sc = t.stride()
+    if c > 1 and sc != 1:
+        raise ValueError(f"{what}: the columns of a row must be adjacent (stride 1), got strides {t.stride()}")
+    if r > 1 and sr < c:
+        raise ValueError(f"{what}: rows overlap (strides {t.stride()})")
+    return sr if r > 1 else c
+
+
+def _vector(t, what, dtype, n, dev):
+    if t.dtype != dtype:
+        raise ValueError(f"{what}: expected {dtype}, got {t.dtype}")
+    if t.dim() != 1 or t.shape[0] != n:
+        raise ValueError(f"{what}: expected shape ({n},), got {tuple(t.shape)}")
+    _on(t, what, dev)
+    if n > 1 and t.stride(0) != 1:
+        raise ValueError(f"{what}: must be contiguous")
+    return t.data_ptr()
+
+
+def _on(t, what, dev):
+    if not t.is_cuda:
+        raise ValueError(f"{what}: tensor must be on a GPU device")
+    if dev is not None and t.device != dev:
+        raise ValueError(f"{what} is on {t.device}, the other tensors on {dev}")
+
+
+def _launch(fn, name, dev, stream, *args):
+    """Call ``fn`` on ``dev`` (made current for the call) and its stream."""
+    import torch
+    if stream is not None and stream.device != dev:
+        raise ValueError(f"the stream is on {stream.device}, the tensors on {dev}")
+    s = torch._C._cuda_getCurrentRawStream(dev.index) if stream is None else stream.cuda_stream
+    if torch.cuda.current_device() == dev.index:
+        rc = fn(*args, s)
+    else:
+        with torch.cuda.device(dev):
+            rc = fn(*args, s)
+    if rc != 1:
+        raise MMQError(f"{name}: {last_error()}")
+
+
+def _codes_out(q, scale, M, K, dev):
+    import torch
+    Kp = _pad16(K)
+    if q is None:
+        q = torch.empty((M, Kp), dtype=torch.int8, device=dev)
+    ldq = _matrix(q, "q", torch.int8, M, Kp, dev)
+    if scale is None:
+        scale = torch.empty((M,), dtype=torch.float32, device=dev)
+    return q, ldq, scale, _vector(scale, "scale", torch.float32, M, dev)
+
+
+def quantize_i8(x, q=None, scale=None, stream=None):
+    """fp32/bf16/fp16 [M, K] -> (int8 codes [M, K rounded up to 16], fp32
+    scales [M]): amax/127 per row (a token, or a weight's output channel).
+    Padding codes are 0; a row with an infinity or NaN gets scale NaN."""
+    dev = x.device
+    code = _type_code(x.dtype)
+    ldx = _matrix(x, "x")
+    M, K = x.shape
+    q, ldq, scale, sp = _codes_out(q, scale, M, K, dev)
+    _launch(lib().mmq_quantize_i8, "mmq_quantize_i8", dev, stream, code, x.data_ptr(), ldx, q.data_ptr(), ldq, sp, M, K)
+    return q, scale
+
+
+def silu_mul_quantize_i8(gate, up, q=None, scale=None, stream=None):
+    """silu(gate) * up ([M, K] each, e.g. the halves of one [M, 2K] matrix),
+    quantized per row as by ``quantize_i8`` -> (codes, scales)."""
+    dev = gate.device
+    code = _type_code(gate.dtype)
+    ld = _matrix(gate, "gate")
+    M, K = gate.shape
+    if _matrix(up, "up", gate.dtype, M, K, dev) != ld:
+        raise ValueError(f"gate and up must have the same row pitch, got strides {gate.stride()} and {up.stride()}")
+    q, ldq, scale, sp = _codes_out(q, scale, M, K, dev)
+    _launch(lib().mmq_silu_mul_quantize_i8, "mmq_silu_mul_quantize_i8", dev, stream, code, gate.data_ptr(),
+            up.data_ptr(), ld, q.data_ptr(), ldq, sp, M, K)
+    return q, scale
+
+
+def _product_out(out, dtype, M, N, dev):
+    import torch
+    if out is None:
+        dtype = torch.float32 if dtype is None else dtype
+        code = _type_code(dtype)
+        return torch.empty((M, N), dtype=dtype, device=dev), code, N
+    if dtype is not None and out.dtype != dtype:
+        raise ValueError(f"out: expected {dtype}, got {out.dtype}")
+    return out, _type_code(out.dtype), _matrix(out, "out", None, M, N, dev)
+
+
+def gemm_i8(xq, xs, wq, ws, bias=None, dtype=None, out=None, stream=None):
+    """Codes [M, K] x codes [N, K] with fp32 scales per token (xs [M]) and per
+    channel (ws [N]), plus an optional fp32 bias [N] -> [M, N] of ``dtype``
+    (float32 by default).  The integer sum is exact."""
+    import torch
+    dev = xq.device
+    ldx = _matrix(xq, "xq", torch.int8)
+    M, K = xq.shape
+    ldw = _matrix(wq, "wq", torch.int8, None, K, dev)
+    N = wq.shape[0]
+    xp = _vector(xs, "xs", torch.float32, M, dev)
+    wp = _vector(ws, "ws", torch.float32, N, dev)
+    bp = None if bias is None else _vector(bias, "bias", torch.float32, N, dev)
+    out, code, ldo = _product_out(out, dtype, M, N, dev)
+    _launch(lib().mmq_gemm_i8, "mmq_gemm_i8", dev, stream, code, xq.data_ptr(), ldx, xp, wq.data_ptr(), ldw, wp, bp,
+            out.data_ptr(), ldo, M, N, K)
+    return out
+
+
+def grouped_gemm_i8(xq, xs, wq, ws, offsets, rows=None, dtype=None, out=None, stream=None):
+    """``gemm_i8`` grouped by expert: output rows offsets[e]..offsets[e+1]-1
+    are codes xq[rows[r]] (xq[r] without ``rows``) times wq[e] ([E, N, K],
+    scales ws [E, N]) -> [R, N], R = len(rows) (or of xq).  ``offsets`` int32
+    [E + 1] and ``rows`` int32 [R] stay on the device.  Rows outside every
+    group, and rows whose index is out of range, are left as they were (in a
+    fresh ``out``: undefined)."""
+    import torch
+    dev = xq.device
+    ldx = _matrix(xq, "xq", torch.int8)
+    T, K = xq.shape
+    if wq.dim() != 3 or wq.dtype != torch.int8:
+        raise ValueError(f"wq: expected int8 [experts, N, K], got {wq.dtype} {tuple(wq.shape)}")
+    E, N, Kw = wq.shape
+    if Kw != K:
+        raise ValueError(f"wq: expected rows of {K} codes, got {Kw}")
+    _on(wq, "wq", dev)
+    if not wq.is_contiguous():
+        raise ValueError("wq must be contiguous")
+    if tuple(ws.shape) != (E, N) or ws.dtype != torch.float32 or not ws.is_contiguous():
+        raise ValueError(f"ws: expected contiguous float32 ({E}, {N}), got {ws.dtype} {tuple(ws.shape)}")
+    _on(ws, "ws", dev)
+    xp = _vector(xs, "xs", torch.float32, T, dev)
+    op = _vector(offsets, "offsets", torch.int32, E + 1, dev)
+    R, rp = T, None
+    if rows is not None:
+        R = rows.numel()
+        rp = _vector(rows, "rows", torch.int32, R, dev)
+    out, code, ldo = _product_out(out, dtype, R, N, dev)
+    _launch(lib().mmq_grouped_gemm_i8, "mmq_grouped_gemm_i8", dev, stream, code, xq.data_ptr(), ldx, xp, T, rp, op, E,
+            wq.data_ptr(), K, ws.data_ptr(), out.data_ptr(), ldo, R, N, K)
+    return out
+
+
+def plan_i8(M, N, K, n_experts=0, cu_count=256) -> tuple[bool, str]:
+    """Pure host planning of ``gemm_i8`` (n_experts 0) or ``grouped_gemm_i8``."""
+    buf = ctypes.create_string_buffer(512)
+    ok = lib().mmq_plan_i8(M, N, K, n_experts, cu_count, buf, 512)
+    return bool(ok), buf.value.decode()
 
 
 def plan_describe(fmt, M, N, K) -> tuple[bool, str]:

@@ -18,8 +18,12 @@
 #include <utility>
 
 #include "../../include/mmq.h"
+#include "i8_plan.hpp"
 #include "mmq_plan.hpp"
 
+static_assert(mmq::TYPE_F32 == MMQ_TYPE_F32 && mmq::TYPE_BF16 == MMQ_TYPE_BF16 && mmq::TYPE_F16 == MMQ_TYPE_F16 &&
+                  mmq::kI8MaxK == MMQ_I8_MAX_K,
+              "header and library disagree");
 static_assert(mmq::kNoAllocMaxRouted == MMQ_MOE_NOALLOC_MAX_ROUTED, "header and library disagree");
 
 namespace mmq {
@@ -32,6 +36,12 @@ hipError_t launch_moe(const Plan &p, const void *x, const void *w, const int32_t
 const void *plan_kernel(const Plan &p, bool dots, bool moe);
 hipError_t noalloc_scratch(void **ptr);
 hipError_t launch_pack_q8_0(const void *w, int64_t N, int64_t K, void *packed, int cu_count, hipStream_t stream);
+hipError_t launch_quantize_i8(int type, const void *x, const void *up, int64_t ldx, void *q, int64_t ldq, float *scale,
+                              int64_t M, int64_t K, hipStream_t stream);
+hipError_t launch_gemm_i8(const I8Plan &p, int type, const void *x, int64_t ldx, const float *xs, int64_t T,
+                          const int32_t *rows, const int32_t *offsets, int experts, const void *w, int64_t ldw,
+                          const float *ws, const float *bias, void *out, int64_t ldo, int64_t M, int64_t N, int64_t K,
+                          hipStream_t stream);
 }  // namespace mmq
 
 namespace {
@@ -491,5 +501,112 @@ int mmq_plan_describe(int fmt, int64_t M, int64_t N, int64_t K, char *buf, int64
 void mmq_debug_set_extra_lds(int64_t extra_bytes) { g_extra_lds.store(extra_bytes < 0 ? 0 : extra_bytes); }
 
 const char *mmq_version(void) { return "mmq-gfx950 0.1"; }
+
+}  // extern "C"
+
+namespace {
+
+// The two row quantizers of the per-token int8 form; `up` null: plain rows.
+int quantize_i8_common(const char *name, int type, const void *x, const void *up, bool silu, int64_t ldx, void *q,
+                       int64_t ldq, float *scale, int64_t M, int64_t K, void *stream) {
+    g_err[0] = '\0';
+    if (!mmq::type_ok(type)) return refuse("unknown type %d", type);
+    if (const char *bad = mmq::check_quantize_i8(M, K, ldx, ldq))
+        return refuse("%s M=%lld K=%lld: %s", name, (long long)M, (long long)K, bad);
+    if (M == 0) return 1;
+    if (!x || (silu && !up) || !q || !scale) return refuse("null pointer argument");
+    if (!aligned(x, mmq::type_bytes(type)) || (silu && !aligned(up, mmq::type_bytes(type))))
+        return refuse("input pointers must be aligned to their type");
+    if (!aligned(q, 16)) return refuse("the codes must be 16-byte aligned");
+    if (!aligned(scale, 4)) return refuse("the scales must be 4-byte aligned");
+    DeviceLimits L;
+    if (!current_limits(&L)) return 0;
+    if (!L.is_gfx950) return refuse("device is %s; this library is built for gfx950 only", L.arch);
+    (void)hipGetLastError();
+    const hipError_t e = mmq::launch_quantize_i8(type, x, silu ? up : nullptr, ldx, q, ldq, scale, M, K,
+                                                 static_cast<hipStream_t>(stream));
+    if (e != hipSuccess) return refuse("%s launch failed: %s", name, hipGetErrorString(e));
+    return 1;
+}
+
+// Dense (experts = 0) or grouped int8 GEMM.
+int gemm_i8_common(const char *name, int type, const void *xq, int64_t ldx, const float *xs, int64_t T,
+                   const int32_t *rows, const int32_t *offsets, int experts, const void *wq, int64_t ldw,
+                   const float *ws, const float *bias, void *out, int64_t ldo, int64_t M, int64_t N, int64_t K,
+                   void *stream) {
+    if (!mmq::type_ok(type)) return refuse("unknown type %d", type);
+    if (const char *bad = mmq::check_gemm_i8(M, N, K, ldx, ldw, ldo))
+        return refuse("%s M=%lld N=%lld K=%lld: %s", name, (long long)M, (long long)N, (long long)K, bad);
+    if (M == 0) return 1;
+    if (!xq || !xs || !wq || !ws || !out) return refuse("null pointer argument");
+    if (!aligned(xq, 16) || !aligned(wq, 16)) return refuse("activation and weight codes must be 16-byte aligned");
+    if (!aligned(xs, 4) || !aligned(ws, 4) || !aligned(bias, 4)) return refuse("scales and bias must be 4-byte aligned");
+    if (!aligned(out, mmq::type_bytes(type))) return refuse("output pointer must be aligned to its type");
+    DeviceLimits L;
+    if (!current_limits(&L)) return 0;
+    if (!L.is_gfx950) return refuse("device is %s; this library is built for gfx950 only", L.arch);
+    mmq::I8Plan p;
+    char why[256];
+    if (!mmq::make_plan_i8(M, N, K, experts, L.cu_count, &p, why, sizeof(why)))
+        return refuse("%s M=%lld N=%lld K=%lld: %s", name, (long long)M, (long long)N, (long long)K, why);
+    (void)hipGetLastError();
+    const hipError_t e = mmq::launch_gemm_i8(p, type, xq, ldx, xs, T, rows, offsets, experts, wq, ldw, ws, bias, out,
+                                             ldo, M, N, K, static_cast<hipStream_t>(stream));
+    if (e != hipSuccess) return refuse("%s launch failed: %s", name, hipGetErrorString(e));
+    return 1;
+}
+
+}  // namespace
+
+extern "C" {
+
+int mmq_quantize_i8(int type, const void *x, int64_t ldx, void *q, int64_t ldq, float *scale, int64_t M, int64_t K,
+                    void *stream) {
+    return quantize_i8_common("int8 quantize", type, x, nullptr, false, ldx, q, ldq, scale, M, K, stream);
+}
+
+int mmq_silu_mul_quantize_i8(int type, const void *gate, const void *up, int64_t ld, void *q, int64_t ldq,
+                             float *scale, int64_t M, int64_t K, void *stream) {
+    return quantize_i8_common("int8 silu-mul quantize", type, gate, up, true, ld, q, ldq, scale, M, K, stream);
+}
+
+int mmq_gemm_i8(int type, const void *xq, int64_t ldx, const float *xs, const void *wq, int64_t ldw, const float *ws,
+                const float *bias, void *out, int64_t ldo, int64_t M, int64_t N, int64_t K, void *stream) {
+    g_err[0] = '\0';
+    return gemm_i8_common("int8 GEMM", type, xq, ldx, xs, M, nullptr, nullptr, 0, wq, ldw, ws, bias, out, ldo, M, N,
+                          K, stream);
+}
+
+int mmq_grouped_gemm_i8(int type, const void *xq, int64_t ldx, const float *xs, int64_t T, const int32_t *rows,
+                        const int32_t *offsets, int n_experts, const void *wq, int64_t ldw, const float *ws, void *out,
+                        int64_t ldo, int64_t R, int64_t N, int64_t K, void *stream) {
+    g_err[0] = '\0';
+    if (n_experts < 1 || n_experts > mmq::kI8MaxExperts)
+        return refuse("grouped int8 GEMM: n_experts must be 1..%d", mmq::kI8MaxExperts);
+    if (T < 0 || T > INT32_MAX) return refuse("grouped int8 GEMM: T must be 0..2^31-1");
+    if (!rows && T < R)
+        return refuse("grouped int8 GEMM: %lld input rows for %lld output rows and no row index", (long long)T,
+                      (long long)R);
+    if (rows && T < 1 && R > 0) return refuse("grouped int8 GEMM: no input rows to gather from");
+    if (R > 0 && !offsets) return refuse("null pointer argument");
+    if (!aligned(rows, 4) || !aligned(offsets, 4)) return refuse("rows and offsets must be 4-byte aligned");
+    return gemm_i8_common("grouped int8 GEMM", type, xq, ldx, xs, T, rows, offsets, n_experts, wq, ldw, ws, nullptr,
+                          out, ldo, R, N, K, stream);
+}
+
+int mmq_plan_i8(int64_t M, int64_t N, int64_t K, int n_experts, int cu_count, char *buf, int64_t len) {
+    mmq::I8Plan p;
+    char why[256];
+    const char *bad = mmq::check_gemm_i8(M, N, K, mmq::pad16(K), mmq::pad16(K), N);
+    if (!bad && (n_experts < 0 || n_experts > mmq::kI8MaxExperts)) bad = "n_experts must be 0 (dense) or 1..2048";
+    const bool ok = !bad && mmq::make_plan_i8(M, N, K, n_experts, cu_count, &p, why, sizeof(why));
+    if (buf && len > 0) {
+        if (ok)
+            mmq::describe_i8(p, buf, size_t(len));
+        else
+            std::snprintf(buf, size_t(len), "%s", bad ? bad : why);
+    }
+    return ok ? 1 : 0;
+}
 
 }  // extern "C"

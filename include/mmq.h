@@ -322,6 +322,81 @@ int mmq_moe_gemm_routed(int fmt, const void *x_q8_1, const void *w, int n_expert
 int mmq_moe_gemm_noalloc(int fmt, const void *x_q8_1, const void *w, int n_experts, const int32_t *ids, int topk,
                          float *out, int64_t T, int64_t N, int64_t K, void *stream);
 
+/* ---------------------------------------------------------------------------
+ * Per-token / per-channel int8: one fp32 scale per activation row (token) and
+ * one per weight row (output channel), so the integer sum of an output runs
+ * over all of K and the scales are applied once.  (The formats above carry a
+ * scale per 32 values instead.)
+ *
+ * Codes are int8, row-major with a row pitch ld in bytes that is a multiple
+ * of 16 (16-byte aligned base), at most 2^22; scales are fp32 arrays.  K is a
+ * multiple of 16 for the products: the quantizers pad a row's codes with
+ * zeros up to the next multiple of 16, and zeros add nothing, so any length
+ * is multiplied as its padded one.  Bytes of a pitch beyond K (or beyond K
+ * rounded up to 16, for the quantizers' output) are neither read nor written.
+ * K <= MMQ_I8_MAX_K keeps the int32 sum of a row exact for any codes, -128
+ * included.  Sizes of zero rows (M = 0, R = 0) return 1 and launch nothing.
+ * The other conventions are those at the top of this file.
+ * ------------------------------------------------------------------------- */
+#define MMQ_TYPE_F32 0
+#define MMQ_TYPE_BF16 1
+#define MMQ_TYPE_F16 2
+#define MMQ_I8_MAX_K 131056
+
+/* Quantize rows (activations per token, or a weight matrix per channel).
+ *   x: M x K of `type` (MMQ_TYPE_*), row pitch ldx >= K in ELEMENTS, aligned
+ *   to its type; q: M rows of int8 codes, pitch ldq; scale: fp32 [M].
+ * Per row, in fp32: amax = max |x|, d = amax/127 (correctly rounded),
+ * code = round-half-away(x * (1/d)) clamped to [-127, 127] (d = 0, or a d so
+ * small that 1/d overflows, gives all codes 0), scale = d: the rule of
+ * mmq_quantize_q8_1 with the row as the block.  Codes K .. K rounded up to 16
+ * are written 0.  A row that holds an infinity or NaN gets codes 0 and scale
+ * NaN, so that every product of it is NaN.  1 <= K <= MMQ_I8_MAX_K. */
+int mmq_quantize_i8(int type, const void *x, int64_t ldx, void *q, int64_t ldq, float *scale, int64_t M, int64_t K,
+                    void *stream);
+
+/* silu(gate) * up, quantized per row as by mmq_quantize_i8: the pass between
+ * an FFN's (or expert's) gate/up product and its down product, in one
+ * reading of them.  gate, up: M x K of `type`, both with row pitch ld in
+ * elements (gate and up may be the two halves of one M x 2K matrix).  The
+ * value is gate / (1 + exp(-gate)) * up in fp32, not rounded to `type`. */
+int mmq_silu_mul_quantize_i8(int type, const void *gate, const void *up, int64_t ld, void *q, int64_t ldq,
+                             float *scale, int64_t M, int64_t K, void *stream);
+
+/* out[m,n] = xs[m] * ws[n] * sum_k xq[m,k] * wq[n,k] (+ bias[n]).
+ *   xq: M x K codes, pitch ldx; xs: fp32 [M]; wq: N x K codes, pitch ldw; ws:
+ *   fp32 [N]; bias: fp32 [N] or NULL; out: M x N of `type`, row pitch ldo >= N
+ *   in ELEMENTS, aligned to its type, every element of the M x N written.
+ * The sum is exact in int32; it is converted to fp32, multiplied by xs, then
+ * by ws, then bias is added (each rounded to fp32), and the result is rounded
+ * once to `type`: the same bits on every run and whichever kernel the planner
+ * picks. */
+int mmq_gemm_i8(int type, const void *xq, int64_t ldx, const float *xs, const void *wq, int64_t ldw, const float *ws,
+                const float *bias, void *out, int64_t ldo, int64_t M, int64_t N, int64_t K, void *stream);
+
+/* mmq_gemm_i8 grouped by expert: rows offsets[e] .. offsets[e+1]-1 of out are
+ * those of expert e,
+ *   out[r,n] = xs[t] * ws[e][n] * sum_k xq[t,k] * wq[e][n,k],
+ * with t = rows[r], or t = r when rows is NULL.  Groups may be empty and of
+ * any lengths; they stay on the device (the host never reads them).
+ *   xq: T x K codes, pitch ldx; xs: fp32 [T]; rows: int32 [R] or NULL (then
+ *   T >= R); offsets: int32 [n_experts + 1], not decreasing; wq: n_experts
+ *   matrices of N x K codes, row pitch ldw, one after another (N * ldw bytes
+ *   apart); ws: fp32 [n_experts][N]; out: R x N of `type`, pitch ldo.
+ * Rows of out before offsets[0] or from offsets[n_experts] on are left as
+ * they were, and so is a row whose rows[r] lies outside 0..T-1.  Offsets are
+ * clamped to 0..R; with decreasing ones it is unspecified which rows of out
+ * are written, but nothing outside the buffers is read or written.
+ * 1 <= n_experts <= 2048. */
+int mmq_grouped_gemm_i8(int type, const void *xq, int64_t ldx, const float *xs, int64_t T, const int32_t *rows,
+                        const int32_t *offsets, int n_experts, const void *wq, int64_t ldw, const float *ws, void *out,
+                        int64_t ldo, int64_t R, int64_t N, int64_t K, void *stream);
+
+/* Pure host planning of the two products (n_experts = 0: mmq_gemm_i8; else
+ * mmq_grouped_gemm_i8 with M = R) for a device of cu_count compute units:
+ * the kernel, its tile and grid into buf.  Returns as mmq_plan_for_limits. */
+int mmq_plan_i8(int64_t M, int64_t N, int64_t K, int n_experts, int cu_count, char *buf, int64_t len);
+
 /* Test entry: the exact int32 block dots I[m,n,b] through the same staging
  * and matrix-core code as the tiled GEMM of format `fmt` (MMQ_FMT_Q8_0,
  * MMQ_FMT_Q4_K or MMQ_FMT_Q5_K; always the tile kernel, whatever M),
