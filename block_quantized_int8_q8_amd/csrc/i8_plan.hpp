@@ -48,24 +48,68 @@ inline const char *check_gemm_i8(int64_t M, int64_t N, int64_t K, int64_t ldx, i
     return nullptr;
 }
 
+// Kernels of the products: tiles of BM x BN outputs, and the few-rows kernel
+// of 16, 32 or 64 rows of x against 16 weight rows.
+enum I8Kernel : int {
+    I8_TILE_256x256, I8_TILE_128x256, I8_TILE_128x128, I8_TILE_64x128, I8_ROWS_16, I8_ROWS_32, I8_ROWS_64, I8_KERNELS
+};
+struct I8KernelInfo {
+    const char *name;
+    int tile_m, tile_n, threads;
+    // microseconds of one 128-wide k-step of one tile, on a CU that does
+    // nothing else, and of a tile's start and end
+    double step_us, fixed_us;
+};
+constexpr I8KernelInfo kI8Kernels[I8_KERNELS] = {
+    {"tile", 256, 256, 512, 1.35, 10.0}, {"tile", 128, 256, 512, 0.87, 7.0}, {"tile", 128, 128, 512, 0.50, 5.0},
+    {"tile", 64, 128, 256, 0.30, 4.0},   {"rows", 16, 16, 512, 0.0, 0.0},    {"rows", 32, 16, 512, 0.0, 0.0},
+    {"rows", 64, 16, 512, 0.0, 0.0},
+};
+
 struct I8Plan {
-    int tile_m = 0, tile_n = 0, threads = 0;
+    int kernel = 0, tile_m = 0, tile_n = 0, threads = 0;
     int64_t tiles_m = 0, tiles_n = 0;
 };
+
+constexpr int64_t kI8BufBytes = 0xfffff000LL;
+
+// Tiles along the rows: `experts` groups (0: one dense matrix) of M rows in
+// all have at most one partial tile each.
+inline int64_t i8_row_tiles(int64_t M, int experts, int tile_m) {
+    return experts ? M / tile_m + (M < experts ? M : experts) : (M + tile_m - 1) / tile_m;
+}
 
 // M rows in all (grouped: over all experts; experts = 0: one dense matrix).
 // Returns false and says why when the launch cannot be made.
 inline bool make_plan_i8(int64_t M, int64_t N, int64_t K, int experts, int cu_count, I8Plan *p, char *why,
                          size_t why_len) {
-    (void)K;
     if (cu_count < 1) {
         std::snprintf(why, why_len, "device reports no compute units");
         return false;
     }
-    p->tile_m = p->tile_n = 128;
-    p->threads = 256;
-    // a ragged grouping has at most one partial tile per non-empty expert
-    p->tiles_m = experts ? M / p->tile_m + (M < experts ? M : experts) : (M + p->tile_m - 1) / p->tile_m;
+    // rows that share a weight matrix, on average
+    const int64_t per = experts ? (M + experts - 1) / experts : M;
+    if (per <= 64) {
+        p->kernel = per <= 16 ? I8_ROWS_16 : per <= 32 ? I8_ROWS_32 : I8_ROWS_64;
+    } else {
+        const int64_t steps = (K + 127) / 128;
+        double best = 0;
+        for (int v = I8_TILE_256x256; v <= I8_TILE_64x128; v++) {
+            const I8KernelInfo &k = kI8Kernels[v];
+            const int64_t groups = experts ? (M < experts ? M : experts) : 1;
+            const int64_t tiles = groups * ((per + k.tile_m - 1) / k.tile_m) * ((N + k.tile_n - 1) / k.tile_n);
+            const double us = double((tiles + cu_count - 1) / cu_count) * (double(steps) * k.step_us + k.fixed_us);
+            if (v == I8_TILE_256x256 || us < best) {
+                best = us;
+                p->kernel = v;
+            }
+        }
+    }
+    const I8KernelInfo &k = kI8Kernels[p->kernel];
+    p->tile_m = k.tile_m;
+    p->tile_n = k.tile_n;
+    p->threads = k.threads;
+    p->tiles_m = i8_row_tiles(M, experts, p->tile_m);
     p->tiles_n = (N + p->tile_n - 1) / p->tile_n;
     if (p->tiles_m * p->tiles_n > INT32_MAX) {
         std::snprintf(why, why_len, "%lld x %lld output tiles exceed the grid's 2^31 - 1", (long long)p->tiles_m,
@@ -76,8 +120,8 @@ inline bool make_plan_i8(int64_t M, int64_t N, int64_t K, int experts, int cu_co
 }
 
 inline void describe_i8(const I8Plan &p, char *buf, size_t len) {
-    std::snprintf(buf, len, "kernel=tile tile=%dx%d threads=%d tiles=%lldx%lld", p.tile_m, p.tile_n, p.threads,
-                  (long long)p.tiles_m, (long long)p.tiles_n);
+    std::snprintf(buf, len, "kernel=%s tile=%dx%d threads=%d tiles=%lldx%lld", kI8Kernels[p.kernel].name, p.tile_m,
+                  p.tile_n, p.threads, (long long)p.tiles_m, (long long)p.tiles_n);
 }
 
 }  // namespace mmq

@@ -539,6 +539,9 @@ int gemm_i8_common(const char *name, int type, const void *xq, int64_t ldx, cons
         return refuse("%s M=%lld N=%lld K=%lld: %s", name, (long long)M, (long long)N, (long long)K, bad);
     if (M == 0) return 1;
     if (!xq || !xs || !wq || !ws || !out) return refuse("null pointer argument");
+    if (rows && T * ldx > mmq::kI8BufBytes)
+        return refuse("%s: rows gathered by index must lie within 4 GiB (T * ldx = %lld)", name,
+                      (long long)T * ldx);
     if (!aligned(xq, 16) || !aligned(wq, 16)) return refuse("activation and weight codes must be 16-byte aligned");
     if (!aligned(xs, 4) || !aligned(ws, 4) || !aligned(bias, 4)) return refuse("scales and bias must be 4-byte aligned");
     if (!aligned(out, mmq::type_bytes(type))) return refuse("output pointer must be aligned to its type");
