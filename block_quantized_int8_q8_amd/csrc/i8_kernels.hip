@@ -16,6 +16,8 @@
 #include <hip/hip_fp16.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "i8_plan.hpp"
 
 namespace mmq {
@@ -123,33 +125,8 @@ typedef __attribute__((address_space(3))) void lds_void;
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t wide_rsrc(const uint8_t *base) {
     return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t *>(base), (short)0, int(kBufBytes), 0x00020000);
 }
-// 16 bytes per lane, global memory to LDS without registers: lane i's bytes
-// land at lds + 16 i.
-__device__ __forceinline__ void dma16(__amdgpu_buffer_rsrc_t r, uint8_t *lds, uint32_t off, int soff) {
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void *)lds, 16, int(off), soff, 0, 0);
-}
 __device__ __forceinline__ i32x4 load16(__amdgpu_buffer_rsrc_t r, uint32_t off, int soff) {
     return __builtin_bit_cast(i32x4, __builtin_amdgcn_raw_buffer_load_b128(r, int(off), soff, 0));
-}
-
-// This wave's DMA has landed, and after the barrier every wave's has.  (The
-// barrier alone orders LDS traffic but does not wait for DMA.)
-__device__ __forceinline__ void dma_barrier() {
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-    __syncthreads();
-}
-
-// Workgroups are dealt to the 8 XCDs in turn, and each XCD has an L2 of its
-// own: hand every XCD a contiguous run of tiles instead, which walks bands of
-// kBand row tiles column by column, so that the tiles in flight on an XCD
-// share operand rows in its L2.
-constexpr int kBand = 8;
-__device__ __forceinline__ void tile_of_block(int tiles_m, int tiles_n, int &tm, int &tn) {
-    const int n = gridDim.x, per = n / 8, rem = n % 8, xcd = blockIdx.x % 8;
-    const int t = xcd * per + min(xcd, rem) + blockIdx.x / 8;
-    const int size = kBand * tiles_n, b = t / size, r = t % size, h = min(kBand, tiles_m - b * kBand);
-    tm = b * kBand + r % h;
-    tn = r / h;
 }
 
 // Row of x that output row m reads; -1: the row is not to be written.
@@ -170,200 +147,391 @@ __device__ __forceinline__ O scaled(int sum, float xs, float ws, float bias, boo
 }
 
 // ---------------------------------------------------------------------------
-// Tile kernel: BM x BN outputs per workgroup of WM x WN waves.
+// Tile kernel: BM x BN outputs per tile, WM x WN waves, NS stages in LDS.
 //
-// Each k-step stages 128 bytes of every row of both operands by DMA into one
-// of two LDS buffers.  A 32-byte sub-step of a wave's tile takes AI + BJ
-// fragment reads (ds_read_b128: row lane % 32, 16-byte half lane / 32) and
-// AI * BJ v_mfma_i32_32x32x32_i8.  The pipeline runs one sub-step ahead in
-// registers and two k-steps ahead in memory: while the matrix core works on
-// sub-step s the fragments of s + 1 are read; the step's barrier stands
-// before its last sub-step, whose fragments are in registers by then, so the
-// buffer is free for step ks + 2's DMA and the next step's first fragments
-// load under the last sub-step's products.  The interleaving of reads, DMA
-// and products is pinned with scheduling groups (left alone, the compiler
-// sinks the reads behind the products: 8192 x 8192 x 8192 466 us against 450).
+// A k-step is 128 bytes of every row of both operands, brought to LDS by DMA
+// NS steps ahead.  The matrix instruction is v_mfma_i32_32x32x32_i8 with
+// A = weights and B = activations, so that a lane's accumulator registers
+// hold four consecutive columns of one output row.
+//
+// What bounds it.  Built without its products the kernel moves tiles at
+// 12-14 TB/s out of the L2s, of which a quarter misses them; without its DMA
+// it runs at 3.6 POP/s; both together, at the full chip's power-limited clock
+// (1.7-2.0 GHz under this load), it reaches 2.1.  So the schedule has to keep
+// loads in flight all the time and let no wave wait for LDS:
+//
+//  - A step's products run in two phases, first half of the tile's rows, then
+//    the second, and the weights' fragments of the whole step stay in
+//    registers between them.  The weights' and the first rows' buffers are
+//    therefore free half a step before the second rows': their DMA for step
+//    ks + NS goes out half a step earlier, which makes NS - 1/2 steps of
+//    lead out of NS buffers (8192 x 18944 x 3584: 543 -> 521 us; one
+//    256 x 256 tile per CU, K = 18944: 222 -> 176 us).
+//  - A cluster is one 32-byte sub-step of one phase.  The fragments of the
+//    next cluster are read behind the products of this one, and the DMA
+//    instructions are spread over the clusters after the barrier that frees
+//    their buffer.  The order is written out and pinned (left alone, the
+//    compiler sinks the reads behind the products).
+//  - DMA is issued and counted by hand.  The compiler cannot tell which LDS
+//    buffer an LDS read depends on and would drain every DMA before it.
+//    vmcnt retires in order, every step issues the same number of DMA
+//    instructions (past the last step they fetch nothing), so "all but the
+//    youngest (NS - 1) * U" names exactly the group a phase needs.
+//  - Workgroups stay: each walks the tiles of its share, and the next tile's
+//    first steps are under way while the last tile is scaled and written.
 //
 // LDS rows are 128 bytes; the eight 16-byte chunks of row r are stored at
 // chunk ^ ((r / 2) % 8), so the 16 lanes that a ds_read_b128 serves at once
-// (16 rows, one chunk) cover all 64 banks.  A DMA instruction writes 1 KiB of
-// LDS in lane order, eight rows; choosing each lane's source chunk realises
-// the order.  Rows past an operand's end repeat its last row (never stored);
-// chunks past K read as zero.
+// (16 rows, one chunk) cover all 64 banks; choosing each DMA lane's source
+// chunk realises the order.  Rows past an operand's end repeat its last row
+// (never stored); chunks past K read as zero.
 //
-// A = weights, B = activations, so a lane's accumulator registers hold four
-// consecutive columns of one output row.  The epilogue scales them, passes
-// each 32-row slab through LDS and stores 16 bytes per lane, 128 contiguous
-// bytes per row.
+// The epilogue scales the accumulators, passes 32-row slabs through LDS and
+// stores 16 bytes per lane, 128 contiguous bytes per row (stored straight
+// from the registers, 32 bytes per row, 2048 x 3584 x 3584 took 35.1 us
+// instead of 31.5).  A slab lies where the wave's own DMA of the last stage
+// goes, and that stage is requested after it.
 // ---------------------------------------------------------------------------
-template <int BM, int BN, int WM, int WN, typename O, bool GROUPED>
-__global__ __launch_bounds__(64 * WM * WN, 2) void k_i8_tile(I8Args a, int tiles_m, int tiles_n) {
-    constexpr int W = WM * WN, AI = BM / WM / 32, BJ = BN / WN / 32, BK = 128;
-    constexpr int UA = BM / 8 / W, UB = BN / 8 / W;      // DMA instructions per wave and k-step
-    constexpr int OFF_W = BM * BK;
-    static_assert(UA * 8 * W == BM && UB * 8 * W == BN && (UA == 1 || UA % 2 == 0) && (UB == 1 || UB % 2 == 0), "staging map");
-    static_assert((BM + BN) * BK >= W * 4096 && (BM + BN) * BK >= (2 * BM + 2 * BN) * 4, "the epilogue reuses the buffers");
-    // two variables: the compiler then sees that reads of one do not wait for DMA into the other
-    __shared__ __align__(16) uint8_t S0[(BM + BN) * BK], S1[(BM + BN) * BK];
-    const int tid = threadIdx.x, lane = tid & 63, wv = __builtin_amdgcn_readfirstlane(tid >> 6);
-    int tm, tn;
-    tile_of_block(tiles_m, tiles_n, tm, tn);
-    int e = 0, row0 = tm * BM, end = int(a.M);
-    if (GROUPED && !find_group<BM>(a.offsets, a.E, int(a.M), tm, e, row0, end)) return;
-    const int n0 = tn * BN, K = int(a.K), N = int(a.N);
-    const bool gather = GROUPED && a.rows;
 
-    const __amdgpu_buffer_rsrc_t rx = wide_rsrc(a.x + (gather ? 0 : int64_t(row0) * a.ldx));
-    const __amdgpu_buffer_rsrc_t rw = wide_rsrc(a.w + (int64_t(e) * a.N + n0) * a.ldw);
-    // lane -> row lane / 8 of its instruction's eight, stored chunk lane % 8
-    const int chunk = 16 * ((lane & 7) ^ (lane >> 4));   // of an even instruction; an odd one's differs in bit 6
-    uint32_t va[UA], vb[UB];
-#pragma unroll
-    for (int u = 0; u < UA; u++) {
-        const int r = min((wv * UA + u) * 8 + (lane >> 3), end - row0 - 1);
-        const uint32_t src = gather ? uint32_t(max(source_row<GROUPED>(a, row0 + r), 0)) : uint32_t(r);
-        va[u] = src * uint32_t(a.ldx) + (chunk ^ (((wv * UA + u) & 1) * 64));
+// 16 (4) bytes per lane from `r` + off + soff to LDS byte address lds + 16 i
+// (4 i) of lane i.  The LDS address is the wave's, not the lane's.
+__device__ __forceinline__ void dma16(i32x4 r, uint32_t lds, uint32_t off, int soff) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds" ::"s"(lds), "v"(off),
+                 "s"(r), "s"(soff)
+                 : "memory", "m0");
+}
+__device__ __forceinline__ void dma4(i32x4 r, uint32_t lds, uint32_t off) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds" ::"s"(lds), "v"(off), "s"(r)
+                 : "memory", "m0");
+}
+// All but this wave's N youngest memory instructions are done, and its LDS
+// reads; after the barrier that holds for every wave.
+template <int N>
+__device__ __forceinline__ void wait_dma() {
+    static_assert(N < 64, "vmcnt holds six bits");
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
+}
+// The descriptor of wide_rsrc, in scalar registers.
+__device__ __forceinline__ i32x4 wide_words(const void *base) {
+    const uint64_t b = reinterpret_cast<uint64_t>(base);
+    return i32x4{__builtin_amdgcn_readfirstlane(int(uint32_t(b))),
+                 __builtin_amdgcn_readfirstlane(int(uint32_t(b >> 32) & 0xffffu)), int(kBufBytes), 0x00020000};
+}
+__device__ __forceinline__ uint32_t lds_address(const void *p) {
+    return uint32_t(reinterpret_cast<uintptr_t>((lds_void *)p));
+}
+
+template <int N, typename F>
+__device__ __forceinline__ void unrolled(F f) {
+    if constexpr (N > 0) {
+        unrolled<N - 1>(f);
+        f(std::integral_constant<int, N - 1>{});
     }
+}
+template <int V> using constant = std::integral_constant<int, V>;
+
+// Row tiles of every expert: start[e] becomes the first tile of expert e, the
+// sum is returned.  Bounds are clamped to [0, M]: no offsets make the kernel
+// leave its buffers.
+template <int TM, int THREADS>
+__device__ __forceinline__ int scan_groups(const I8Args &a, int *start, int *part) {
+    const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6, M = int(a.M);
+    int carry = 0;
+    for (int e0 = 0; e0 < a.E; e0 += THREADS) {
+        const int e = e0 + tid;
+        int n = 0;
+        if (e < a.E) {
+            const int b = min(max(a.offsets[e], 0), M), t = min(max(a.offsets[e + 1], 0), M);
+            n = t > b ? (t - b + TM - 1) / TM : 0;
+        }
+        int upto = n;
 #pragma unroll
-    for (int u = 0; u < UB; u++)
-        vb[u] = uint32_t(min((wv * UB + u) * 8 + (lane >> 3), N - n0 - 1)) * uint32_t(a.ldw) +
-                (chunk ^ (((wv * UB + u) & 1) * 64));
-    const int steps = (K + BK - 1) / BK;
-    auto load = [&](int ks, uint8_t *S) {                // past the last step: fetches nothing
-        const int k0 = ks * BK;
-        const bool in0 = k0 + chunk < K, in1 = k0 + (chunk ^ 64) < K;
+        for (int o = 1; o < 64; o <<= 1) {
+            const int v = __shfl_up(upto, o);
+            if (lane >= o) upto += v;
+        }
+        if (lane == 63) part[wv] = upto;
+        __syncthreads();
+        int before = carry, sum = 0;
 #pragma unroll
-        for (int u = 0; u < UA; u++)
-            dma16(rx, S + (wv * UA + u) * 1024, (((wv * UA + u) & 1) ? in1 : in0) ? va[u] : kNowhere, k0);
+        for (int w = 0; w < THREADS / 64; w++) {
+            if (w < wv) before += part[w];
+            sum += part[w];
+        }
+        if (e < a.E) start[e] = before + upto - n;
+        carry += sum;
+        __syncthreads();
+    }
+    return __builtin_amdgcn_readfirstlane(carry);
+}
+// The expert of row tile `tile`: the last e with start[e] <= tile (of equal
+// starts only the last has tiles).  64-way search by one wave.
+__device__ __forceinline__ int group_of(const int *start, int E, int tile) {
+    const int lane = threadIdx.x & 63;
+    int lo = 0, n = E;
+    while (n > 1) {
+        const int stride = (n + 63) / 64;
+        const bool ok = lane * stride < n && start[lo + lane * stride] <= tile;
+        const int c = __popcll(__ballot(ok)) - 1;
+        lo += c * stride;
+        n = min(stride, n - c * stride);
+    }
+    return __builtin_amdgcn_readfirstlane(lo);
+}
+
+// Workgroups are dealt to the 8 XCDs in turn, and each XCD has an L2 of its
+// own: every XCD gets a contiguous run of tiles, which walks bands of kBand
+// row tiles column by column, so that the tiles in flight on an XCD share
+// operand rows in its L2.  Measured at 8192 x 18944 x 3584 (256 x 256 /
+// 128 x 256 tiles): bands of 4 527 / 577 us, 6 512 / 554, 8 524 / 593,
+// 16 527 / 593.
+constexpr int kBand = 6;
+
+template <int BM, int BN, int WM, int WN, int NS, int OCC, typename O, bool GROUPED>
+__global__ __launch_bounds__(64 * WM * WN, OCC) void k_i8_tile(I8Args a, int tiles_m, int tiles_n) {
+    constexpr int W = WM * WN, AI = BM / WM / 32, BJ = BN / WN / 32, BK = 128, SUB = BK / 32;
+    constexpr int UA = BM / 8 / W, UB = BN / 8 / W, U = UA + UB;   // DMA instructions (8 rows) per wave and step
+    constexpr int AH = AI / 2, UH = UA / 2, G1 = UB + UH;          // ... of phase 0: the weights and half the rows
+    constexpr int HW = BM / WM / 2;                                // rows of a wave's tile in one half
+    constexpr int OFF_W = BM * BK, STAGE = (BM + BN) * BK, SCALES = BM + 2 * BN;
+    static_assert(UA * 8 * W == BM && UB * 8 * W == BN && AI % 2 == 0 && UA % 2 == 0, "staging map");
+    __shared__ __align__(1024) uint8_t S[NS * STAGE];
+    __shared__ __align__(16) float scales[2][SCALES];              // xs, ws, bias of this tile and the next
+    __shared__ int start[GROUPED ? kI8MaxExperts : 1], part[W];
+    const int tid = threadIdx.x, lane = tid & 63, wv = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int K = int(a.K), N = int(a.N), steps = (K + BK - 1) / BK;
+    const bool gather = GROUPED && a.rows, has_bias = a.bias != nullptr;
+    const uint32_t lds0 = lds_address(S), lds_scales = lds_address(scales);
+    const int wm = (wv / WN) * 2 * HW, wn = (wv % WN) * (BN / WN), h = lane >> 5, ml = lane & 31;
+
+    if (GROUPED) tiles_m = scan_groups<BM, 64 * W>(a, start, part);
+    // this workgroup's tiles: every nb-th of its XCD's share
+    const int total = tiles_m * tiles_n, xcd = blockIdx.x % 8, nb = (int(gridDim.x) - xcd + 7) / 8;
+    int t = xcd * (total / 8) + min(xcd, total % 8) + blockIdx.x / 8;
+    const int t_end = (xcd + 1) * (total / 8) + min(xcd + 1, total % 8);
+    if (t >= t_end) return;
+
+    // source chunk of this lane in DMA instruction u of an operand
+    auto chunk_of = [&](int u) { return 16 * ((lane & 7) ^ (((u * 8 + (lane >> 3)) >> 1) & 7)); };
+    int row0, end, e, n0, stored;          // stored: bit i, this lane's row of sub-tile i exists
+    i32x4 rx, rw;
+    uint32_t va[UA], vb[UB];
+    auto setup = [&]() {                   // tile t
+        const int size = kBand * tiles_n, b = t / size, r = t % size, hb = min(kBand, tiles_m - b * kBand);
+        const int tm = b * kBand + r % hb;
+        n0 = (r / hb) * BN;
+        e = 0;
+        row0 = tm * BM;
+        end = int(a.M);
+        if (GROUPED) {
+            typedef const __attribute__((address_space(4))) int *scalar_ints;
+            const scalar_ints off = (scalar_ints)a.offsets;
+            e = group_of(start, a.E, tm);
+            row0 = min(max(off[e], 0), end) + (tm - __builtin_amdgcn_readfirstlane(start[e])) * BM;
+            end = min(max(off[e + 1], 0), end);
+        }
+        rx = wide_words(a.x + (gather ? 0 : int64_t(row0) * a.ldx));
+        rw = wide_words(a.w + (int64_t(e) * N + n0) * a.ldw);
+#pragma unroll
+        for (int u = 0; u < UA; u++) {     // LDS holds the halves one after the other
+            const int rh = (wv * UH + u % UH) * 8 + (lane >> 3);
+            const int r = min((rh / HW) * 2 * HW + (u / UH) * HW + rh % HW, end - row0 - 1);
+            const uint32_t src = gather ? uint32_t(max(source_row<GROUPED>(a, row0 + r), 0)) : uint32_t(r);
+            va[u] = src * uint32_t(a.ldx) + chunk_of(wv * UH + u % UH);
+        }
 #pragma unroll
         for (int u = 0; u < UB; u++)
-            dma16(rw, S + OFF_W + (wv * UB + u) * 1024, (((wv * UB + u) & 1) ? in1 : in0) ? vb[u] : kNowhere, k0);
+            vb[u] = uint32_t(min((wv * UB + u) * 8 + (lane >> 3), N - n0 - 1)) * uint32_t(a.ldw) + chunk_of(wv * UB + u);
+        stored = 0;
+#pragma unroll
+        for (int i = 0; i < AI; i++) {
+            const int m = row0 + wm + 32 * i + ml;
+            if (m < end && source_row<GROUPED>(a, m) >= 0) stored |= 1 << i;
+        }
+    };
+    // Instruction u of a step: UB of the weights, UH of the first rows, UH of
+    // the second.  Chunks past K, and so whole steps past the last, fetch
+    // nothing.
+    auto load1 = [&](int u, int k0, int stage) {
+        if (u < UB) {
+            const bool in = k0 + chunk_of(wv * UB + u) < K;
+            dma16(rw, lds0 + stage * STAGE + OFF_W + (wv * UB + u) * 1024, in ? vb[u < UB ? u : 0] : kNowhere, k0);
+        } else {
+            const int v = u - UB;
+            const bool in = k0 + chunk_of(wv * UH + v % UH) < K;
+            dma16(rx, lds0 + stage * STAGE + (v / UH) * (OFF_W / 2) + (wv * UH + v % UH) * 1024,
+                  in ? va[v >= 0 && v < UA ? v : 0] : kNowhere, k0);
+        }
+    };
+    auto load = [&](int ks, int stage, int u0, int u1) {
+#pragma unroll
+        for (int u = 0; u < U; u++)
+            if (u >= u0 && u < u1) load1(u, ks * BK, stage);
+    };
+    auto load_scales = [&](int parity) {   // 64 values an instruction, dealt to the waves
+        const i32x4 rs = wide_words(a.xs + (gather ? 0 : row0)), rv = wide_words(a.ws + int64_t(e) * N + n0);
+        const i32x4 rb = wide_words(a.bias + n0);
+        const uint32_t base = lds_scales + parity * SCALES * 4;
+        for (int g = wv; g < BM / 64; g += W) {
+            const int r = g * 64 + lane, src = row0 + r >= end ? -1 : gather ? source_row<GROUPED>(a, row0 + r) : r;
+            dma4(rs, base + g * 256, src < 0 ? kNowhere : uint32_t(src) * 4);
+        }
+        for (int g = W - 1 - wv; g < BN / 64; g += W) {
+            const uint32_t off = n0 + g * 64 + lane < N ? uint32_t(g * 64 + lane) * 4 : kNowhere;
+            dma4(rv, base + BM * 4 + g * 256, off);
+            if (has_bias) dma4(rb, base + (BM + BN) * 4 + g * 256, off);
+        }
     };
 
-    i32x16 acc[AI][BJ] = {};
-    const int wm = (wv / WN) * (BM / WM), wn = (wv % WN) * (BN / WN), h = lane >> 5;
-    const int a_off = (wm + (lane & 31)) * BK, b_off = OFF_W + (wn + (lane & 31)) * BK;
-    int co[4];                                           // sub-step s: this lane's chunk
+    i32x16 acc[AI][BJ];
+    const int a_off = ((wv / WN) * HW + ml) * BK, b_off = OFF_W + (wn + ml) * BK;
+    int co[SUB];                           // this lane's chunk of sub-step s: row lane % 32, half lane / 32
 #pragma unroll
-    for (int s = 0; s < 4; s++) co[s] = 16 * ((2 * s + h) ^ ((lane >> 1) & 7));
-    i32x4 fa[2][AI], fb[2][BJ];
-    auto frags = [&](const uint8_t *S, int s, int p) {
-#pragma unroll
-        for (int j = 0; j < BJ; j++) fb[p][j] = *reinterpret_cast<const i32x4 *>(S + b_off + co[s] + 32 * BK * j);
-#pragma unroll
-        for (int i = 0; i < AI; i++) fa[p][i] = *reinterpret_cast<const i32x4 *>(S + a_off + co[s] + 32 * BK * i);
+    for (int s = 0; s < SUB; s++) co[s] = 16 * ((2 * s + h) ^ ((lane >> 1) & 7));
+    i32x4 fa[2][AH], fb[SUB][BJ];
+    auto frag_b = [&](int j, int stage, int s) {
+        fb[s][j] = *reinterpret_cast<const i32x4 *>(S + stage * STAGE + b_off + co[s] + 32 * BK * j);
     };
-    auto mma = [&](int p) {
-#pragma unroll
-        for (int i = 0; i < AI; i++)
-#pragma unroll
-            for (int j = 0; j < BJ; j++)
-                acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fb[p][j], fa[p][i], acc[i][j], 0, 0, 0);
+    auto frag_a = [&](int i, int stage, int half, int s, int p) {
+        fa[p][i] = *reinterpret_cast<const i32x4 *>(S + stage * STAGE + half * (OFF_W / 2) + a_off + co[s] + 32 * BK * i);
     };
-    // scheduling groups: 0x008 products, 0x100 LDS reads, 0x010 memory instructions
-    constexpr int NR = AI + BJ, NM = AI * BJ, REST = NM > NR ? NM - NR : 1;
-    constexpr int QR = (NR + 1) / 2, QD = NM > QR ? NM - QR : 1, VP = (UA + UB + QD - 1) / QD;
-    auto step = [&](int ks, uint8_t *cur, const uint8_t *nxt) {
-#pragma unroll
-        for (int s = 0; s < 3; s++) {
-            frags(cur, s + 1, (s + 1) & 1);
-            mma(s & 1);
-#pragma unroll
-            for (int q = 0; q < NR; q++) {
-                __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-                __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
-            }
-            __builtin_amdgcn_sched_group_barrier(0x008, REST, 0);
-            __builtin_amdgcn_sched_barrier(0);
-        }
-        dma_barrier();                                   // step ks + 1 has landed; `cur` is in registers
-        frags(nxt, 0, 0);
-        load(ks + 2, cur);
-        mma(1);
+    // Products of row half HALF and sub-step SS; behind them the reads of the
+    // next cluster's fragments (stage rstage) and DMA instructions D0 .. D1-1
+    // of the step at k0 into dstage.
+    auto cluster = [&](auto half_, auto s_, int rstage, auto d0_, auto d1_, int k0, int dstage) {
+        constexpr int HALF = decltype(half_)::value, SS = decltype(s_)::value, P = SS & 1;
+        constexpr int D0 = decltype(d0_)::value, ND = decltype(d1_)::value - D0, NM = AH * BJ;
+        constexpr int NSUB = (SS + 1) % SUB, NHALF = SS + 1 < SUB ? HALF : 1 - HALF;
+        constexpr int NB = NHALF == 0 ? BJ : 0, NR = AH + NB;      // phase 1 has the weights in registers
 #pragma unroll
         for (int q = 0; q < NM; q++) {
-            __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-            if (q < QR)
-                __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
-            else
-                __builtin_amdgcn_sched_group_barrier(0x010, VP, 0);
-        }
-        __builtin_amdgcn_sched_barrier(0);
-    };
-    load(0, S0);
-    load(1, S1);
-    dma_barrier();
-    int ks = 0;
-    if (row0 + wm < end) {
-        frags(S0, 0, 0);
-        for (; ks + 1 < steps; ks += 2) {
-            step(ks, S0, S1);
-            step(ks + 1, S1, S0);
-        }
-        if (ks < steps) step(ks, S0, S1);
-    } else {                                             // no rows of this wave's tile exist: staging only
-        for (; ks < steps; ks++) {
-            dma_barrier();
-            load(ks + 2, ks & 1 ? S1 : S0);
-        }
-    }
-    dma_barrier();
-
-    float *sxs = reinterpret_cast<float *>(S1), *sws = sxs + BM, *sbias = sws + BN;
-    int *sdst = reinterpret_cast<int *>(sbias + BN);     // output row of each tile row, -1: none
-    for (int r = tid; r < BM; r += 64 * W) {
-        const int m = row0 + r, src = m < end ? source_row<GROUPED>(a, m) : -1;
-        sdst[r] = src < 0 ? -1 : m;
-        sxs[r] = src < 0 ? 0.0f : a.xs[src];
-    }
-    const bool has_bias = a.bias != nullptr;
-    for (int r = tid; r < BN; r += 64 * W) {
-        sws[r] = n0 + r < N ? a.ws[int64_t(e) * a.N + n0 + r] : 0.0f;
-        if (has_bias) sbias[r] = n0 + r < N ? a.bias[n0 + r] : 0.0f;
-    }
-    __syncthreads();
-    if (row0 + wm >= end) return;
-    // GJ sub-tiles side by side fill 128-byte slab rows of CH chunks, stored swizzled
-    constexpr int GJ = sizeof(O) == 2 && BJ % 2 == 0 ? 2 : 1, CH = GJ * 2 * int(sizeof(O)), PER = 16 / int(sizeof(O));
-    uint8_t *slab = S0 + wv * 4096;
-    O *out = static_cast<O *>(a.out);
-    const int ml = lane & 31;
+            i32x16 &c = acc[HALF * AH + q / BJ][q % BJ];
+            c = __builtin_amdgcn_mfma_i32_32x32x32_i8(fb[SS][q % BJ], fa[P][q / BJ], c, 0, 0, 0);
 #pragma unroll
-    for (int i = 0; i < AI; i++) {
-        const float xs = sxs[wm + 32 * i + ml];
-#pragma unroll
-        for (int jj = 0; jj < BJ / GJ; jj++) {
-#pragma unroll
-            for (int g = 0; g < GJ; g++)
-#pragma unroll
-                for (int q = 0; q < 4; q++) {
-                    const int j = jj * GJ + g, c = wn + 32 * j + 8 * q + 4 * h;
-                    struct alignas(4 * sizeof(O)) { O v[4]; } o;
-#pragma unroll
-                    for (int r = 0; r < 4; r++)
-                        o.v[r] = scaled<O>(acc[i][j][4 * q + r], xs, sws[c + r], has_bias ? sbias[c + r] : 0.0f, has_bias);
-                    const int at = sizeof(O) == 2 ? 16 * ((4 * g + q) ^ (ml & (CH - 1))) + 8 * h
-                                                  : 16 * ((2 * q + h) ^ (ml & (CH - 1)));
-                    __builtin_memcpy(__builtin_assume_aligned(slab + ml * CH * 16 + at, 4 * sizeof(O)), &o, sizeof(o));
+            for (int r = 0; r < NR; r++)
+                if (r * NM / NR == q) {                            // b0 a0 a1 .. b1 ..: as the products need them
+                    const int ra = r - (NB ? 1 : 0);
+                    if (NB && r == 0)
+                        frag_b(0, rstage, NSUB);
+                    else if (ra < AH)
+                        frag_a(ra, rstage, NHALF, NSUB, 1 - P);
+                    else
+                        frag_b(r - AH, rstage, NSUB);
                 }
 #pragma unroll
-            for (int it = 0; it < CH / 2; it++) {
-                const int row = it * (64 / CH) + lane / CH, c = lane % CH;
-                const i32x4 v = *reinterpret_cast<const i32x4 *>(slab + row * CH * 16 + 16 * (c ^ (row & (CH - 1))));
-                const int dst = sdst[wm + 32 * i + row], n = n0 + wn + 32 * GJ * jj + c * PER;
-                if (dst >= 0) {
-                    O *o = out + int64_t(dst) * a.ldo + n;
-                    if (n + PER <= N)
-                        __builtin_memcpy(o, &v, 16);     // rows may start at any multiple of the type's size
-                    else {
-                        const O *ov = reinterpret_cast<const O *>(&v);
+            for (int d = 0; d < ND; d++)
+                if (d * NM / (ND > 0 ? ND : 1) == q) load1(D0 + d, k0, dstage);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+    };
+    auto step = [&](int ks, auto stage_) {
+        constexpr int STG = decltype(stage_)::value, NXT = (STG + 1) % NS;
+        const int k2 = (ks + NS) * BK;
+        unrolled<SUB - 1>([&](auto s) { cluster(constant<0>{}, s, STG, constant<0>{}, constant<0>{}, 0, 0); });
+        // the second rows have landed; the weights and the first rows are in registers
+        wait_dma<(NS - 1) * U>();
+        constexpr int D1 = (G1 + 3) / 4, D2 = D1 + (G1 - D1 + 2) / 3, D3 = D2 + (G1 - D2 + 1) / 2;
+        cluster(constant<0>{}, constant<3>{}, STG, constant<0>{}, constant<D1>{}, k2, STG);
+        cluster(constant<1>{}, constant<0>{}, STG, constant<D1>{}, constant<D2>{}, k2, STG);
+        cluster(constant<1>{}, constant<1>{}, STG, constant<D2>{}, constant<D3>{}, k2, STG);
+        cluster(constant<1>{}, constant<2>{}, STG, constant<D3>{}, constant<G1>{}, k2, STG);
+        // the next step's weights and first rows have landed; the second rows are in registers
+        wait_dma<(NS - 1) * U>();
+        cluster(constant<1>{}, constant<3>{}, NXT, constant<G1>{}, constant<U>{}, k2, STG);
+    };
+
+    constexpr int PER = 16 / int(sizeof(O)), STORES = AI * BJ * 32 * 32 / (64 * PER);   // 16-byte stores per wave and tile
+    constexpr int RB = UB >= 4 && BJ * 32 * sizeof(O) >= 128 ? 128 : 64, CH = RB / 16;  // slab row: bytes, chunks
+    constexpr int CW = RB / int(sizeof(O));                                             // and columns
+    static_assert(32 * RB <= UB * 1024, "a slab fits the wave's own DMA destination");
+    setup();
+    unrolled<NS>([&](auto i) { load(i, i, 0, U); });
+    load_scales(0);
+    bool full = false;                     // STORES stores are younger than the loads of stages 0 .. NS - 2
+    for (int parity = 0;; parity ^= 1) {
+        if (full)
+            wait_dma<(NS - 1) * U + STORES>();
+        else
+            wait_dma<0>();
+        const bool active = row0 + wm < end;
+        if (active) {
 #pragma unroll
-                        for (int q = 0; q < PER; q++)
-                            if (n + q < N) o[q] = ov[q];
+            for (int i = 0; i < AI; i++)
+#pragma unroll
+                for (int j = 0; j < BJ; j++) acc[i][j] = i32x16{};
+#pragma unroll
+            for (int j = 0; j < BJ; j++) frag_b(j, 0, 0);
+#pragma unroll
+            for (int i = 0; i < AH; i++) frag_a(i, 0, 0, 0, 0);
+            int ks = 0;
+            for (; ks + NS <= steps; ks += NS) unrolled<NS>([&](auto i) { step(ks + i, i); });
+            unrolled<NS - 1>([&](auto i) {
+                if (ks + i < steps) step(ks + i, i);
+            });
+        } else {                           // no rows of this wave's tile exist: staging only
+            for (int ks = 0; ks < steps; ks++) {
+                wait_dma<(NS - 1) * U>();
+                load(ks + NS, ks % NS, 0, G1);
+                wait_dma<(NS - 1) * U>();
+                load(ks + NS, ks % NS, G1, U);
+            }
+        }
+        wait_dma<0>();
+        const int o_row = row0 + wm, o_n = n0 + wn, o_stored = stored;
+        t += nb;
+        const bool more = t < t_end;
+        if (more) {
+            setup();
+            unrolled<NS - 1>([&](auto i) { load(i, i, 0, U); });
+            load_scales(parity ^ 1);
+        }
+        full = false;
+        if (active) {
+            const float *sxs = scales[parity], *sws = sxs + BM, *sbias = sws + BN;
+            O *out = static_cast<O *>(a.out) + int64_t(o_row) * a.ldo + o_n;
+            const int n_left = N - o_n;
+            full = __all(o_stored == (1 << AI) - 1) && BJ * 32 <= n_left;
+            uint8_t *slab = S + (NS - 1) * STAGE + OFF_W + wv * UB * 1024;
+#pragma unroll
+            for (int i = 0; i < AI; i++) {
+                const float xs = sxs[wm + 32 * i + ml];
+#pragma unroll
+                for (int cc = 0; cc < BJ * 32 / CW; cc++) {
+                    asm volatile("" ::: "memory");                 // the scales are read again, not kept in registers
+#pragma unroll
+                    for (int g = 0; g < CW / 8; g++) {             // eight columns, four in each half of the wave
+                        const int j = (cc * CW + 8 * g) / 32, q = (cc * CW / 8 + g) % 4, c = wn + 32 * j + 8 * q + 4 * h;
+                        struct alignas(4 * sizeof(O)) { O v[4]; } o;
+#pragma unroll
+                        for (int r = 0; r < 4; r++)
+                            o.v[r] = scaled<O>(acc[i][j][4 * q + r], xs, sws[c + r], has_bias ? sbias[c + r] : 0.0f, has_bias);
+                        const int at = sizeof(O) == 2 ? 16 * (g ^ (ml & (CH - 1))) + 8 * h : 16 * ((2 * g + h) ^ (ml & (CH - 1)));
+                        __builtin_memcpy(__builtin_assume_aligned(slab + ml * RB + at, 4 * sizeof(O)), &o, sizeof(o));
+                    }
+#pragma unroll
+                    for (int it = 0; it < CH / 2; it++) {
+                        const int row = it * (64 / CH) + lane / CH, ck = lane % CH, n = cc * CW + ck * PER;
+                        const i32x4 v = *reinterpret_cast<const i32x4 *>(slab + row * RB + 16 * (ck ^ (row & (CH - 1))));
+                        O *p = out + int64_t(32 * i + row) * a.ldo + n;
+                        if (full)
+                            __builtin_memcpy(p, &v, 16);           // rows may start at any multiple of the type's size
+                        else if (__shfl(o_stored, row) >> i & 1) {
+                            if (n + PER <= n_left)
+                                __builtin_memcpy(p, &v, 16);
+                            else {
+                                const O *ov = reinterpret_cast<const O *>(&v);
+#pragma unroll
+                                for (int r = 0; r < PER; r++)
+                                    if (n + r < n_left) p[r] = ov[r];
+                            }
+                        }
                     }
                 }
             }
         }
+        if (!more) break;
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");         // the slab has been read
+        load(NS - 1, NS - 1, 0, U);
     }
 }
 
@@ -472,13 +640,13 @@ hipError_t launch_quantize_i8(int type, const void *x, const void *up, int64_t l
 
 template <typename O, bool GROUPED>
 static void launch_kernel(const I8Plan &p, const I8Args &a, hipStream_t stream) {
-    const dim3 grid((unsigned)(p.tiles_m * p.tiles_n));
+    const dim3 grid((unsigned)p.workgroups);
     const int tm = int(p.tiles_m), tn = int(p.tiles_n);
     switch (p.kernel) {
-    case I8_TILE_256x256: k_i8_tile<256, 256, 2, 4, O, GROUPED><<<grid, 512, 0, stream>>>(a, tm, tn); break;
-    case I8_TILE_128x256: k_i8_tile<128, 256, 2, 4, O, GROUPED><<<grid, 512, 0, stream>>>(a, tm, tn); break;
-    case I8_TILE_128x128: k_i8_tile<128, 128, 2, 4, O, GROUPED><<<grid, 512, 0, stream>>>(a, tm, tn); break;
-    case I8_TILE_64x128: k_i8_tile<64, 128, 2, 2, O, GROUPED><<<grid, 256, 0, stream>>>(a, tm, tn); break;
+    case I8_TILE_256x256: k_i8_tile<256, 256, 2, 4, 2, 2, O, GROUPED><<<grid, 512, 0, stream>>>(a, tm, tn); break;
+    case I8_TILE_128x256: k_i8_tile<128, 256, 2, 4, 3, 2, O, GROUPED><<<grid, 512, 0, stream>>>(a, tm, tn); break;
+    case I8_TILE_128x128: k_i8_tile<128, 128, 2, 2, 2, 2, O, GROUPED><<<grid, 256, 0, stream>>>(a, tm, tn); break;
+    case I8_TILE_64x128: k_i8_tile<64, 128, 1, 4, 2, 3, O, GROUPED><<<grid, 256, 0, stream>>>(a, tm, tn); break;
     case I8_ROWS_16: k_i8_rows<1, 1, 4, O, GROUPED><<<grid, 512, 0, stream>>>(a, tm, tn); break;
     case I8_ROWS_32: k_i8_rows<2, 1, 2, O, GROUPED><<<grid, 512, 0, stream>>>(a, tm, tn); break;
     case I8_ROWS_64: k_i8_rows<4, 1, 2, O, GROUPED><<<grid, 512, 0, stream>>>(a, tm, tn); break;

@@ -56,19 +56,20 @@ enum I8Kernel : int {
 struct I8KernelInfo {
     const char *name;
     int tile_m, tile_n, threads;
-    // microseconds of one 128-wide k-step of one tile, on a CU that does
-    // nothing else, and of a tile's start and end
+    int per_cu;                // workgroups resident per CU (tile kernels: their LDS; they walk over the tiles)
+    // microseconds of one 128-wide k-step of one tile, and of a tile's start
+    // and end, with every CU at work (measured at K = 3584 and 18944)
     double step_us, fixed_us;
 };
 constexpr I8KernelInfo kI8Kernels[I8_KERNELS] = {
-    {"tile", 256, 256, 512, 1.35, 10.0}, {"tile", 128, 256, 512, 0.87, 7.0}, {"tile", 128, 128, 512, 0.50, 5.0},
-    {"tile", 64, 128, 256, 0.30, 4.0},   {"rows", 16, 16, 512, 0.0, 0.0},    {"rows", 32, 16, 512, 0.0, 0.0},
-    {"rows", 64, 16, 512, 0.0, 0.0},
+    {"tile", 256, 256, 512, 1, 1.55, 6.0}, {"tile", 128, 256, 512, 1, 0.87, 5.5}, {"tile", 128, 128, 256, 2, 0.51, 3.0},
+    {"tile", 64, 128, 256, 2, 0.30, 2.0},  {"rows", 16, 16, 512, 0, 0.0, 0.0},    {"rows", 32, 16, 512, 0, 0.0, 0.0},
+    {"rows", 64, 16, 512, 0, 0.0, 0.0},
 };
 
 struct I8Plan {
     int kernel = 0, tile_m = 0, tile_n = 0, threads = 0;
-    int64_t tiles_m = 0, tiles_n = 0;
+    int64_t tiles_m = 0, tiles_n = 0, workgroups = 0;
 };
 
 constexpr int64_t kI8BufBytes = 0xfffff000LL;
@@ -96,8 +97,10 @@ inline bool make_plan_i8(int64_t M, int64_t N, int64_t K, int experts, int cu_co
         double best = 0;
         for (int v = I8_TILE_256x256; v <= I8_TILE_64x128; v++) {
             const I8KernelInfo &k = kI8Kernels[v];
-            const int64_t groups = experts ? (M < experts ? M : experts) : 1;
-            const int64_t tiles = groups * ((per + k.tile_m - 1) / k.tile_m) * ((N + k.tile_n - 1) / k.tile_n);
+            // a group's last row tile is half full on average
+            const int64_t groups = experts ? (M < experts ? M : experts) : 0;
+            const int64_t row_tiles = experts ? M / k.tile_m + (groups + 1) / 2 : (M + k.tile_m - 1) / k.tile_m;
+            const int64_t tiles = row_tiles * ((N + k.tile_n - 1) / k.tile_n);
             const double us = double((tiles + cu_count - 1) / cu_count) * (double(steps) * k.step_us + k.fixed_us);
             if (v == I8_TILE_256x256 || us < best) {
                 best = us;
@@ -116,12 +119,14 @@ inline bool make_plan_i8(int64_t M, int64_t N, int64_t K, int experts, int cu_co
                       (long long)p->tiles_n);
         return false;
     }
+    p->workgroups = p->tiles_m * p->tiles_n;
+    if (k.per_cu && p->workgroups > int64_t(cu_count) * k.per_cu) p->workgroups = int64_t(cu_count) * k.per_cu;
     return true;
 }
 
 inline void describe_i8(const I8Plan &p, char *buf, size_t len) {
-    std::snprintf(buf, len, "kernel=%s tile=%dx%d threads=%d tiles=%lldx%lld", kI8Kernels[p.kernel].name, p.tile_m,
-                  p.tile_n, p.threads, (long long)p.tiles_m, (long long)p.tiles_n);
+    std::snprintf(buf, len, "kernel=%s tile=%dx%d threads=%d tiles=%lldx%lld workgroups=%lld", kI8Kernels[p.kernel].name, p.tile_m,
+                  p.tile_n, p.threads, (long long)p.tiles_m, (long long)p.tiles_n, (long long)p.workgroups);
 }
 
 }  // namespace mmq
