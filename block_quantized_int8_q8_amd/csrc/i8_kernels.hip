@@ -122,13 +122,6 @@ constexpr uint32_t kBufBytes = 0xfffff000u, kNowhere = 0xfffff800u;
 static_assert(int64_t(kBufBytes) == kI8BufBytes, "plan and kernel disagree");
 typedef __attribute__((address_space(3))) void lds_void;
 
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t wide_rsrc(const uint8_t *base) {
-    return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t *>(base), (short)0, int(kBufBytes), 0x00020000);
-}
-__device__ __forceinline__ i32x4 load16(__amdgpu_buffer_rsrc_t r, uint32_t off, int soff) {
-    return __builtin_bit_cast(i32x4, __builtin_amdgcn_raw_buffer_load_b128(r, int(off), soff, 0));
-}
-
 // Row of x that output row m reads; -1: the row is not to be written.
 template <bool GROUPED>
 __device__ __forceinline__ int source_row(const I8Args &a, int m) {
@@ -211,7 +204,7 @@ __device__ __forceinline__ void wait_dma() {
     static_assert(N < 64, "vmcnt holds six bits");
     asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
 }
-// The descriptor of wide_rsrc, in scalar registers.
+// Such a buffer's descriptor, in scalar registers.
 __device__ __forceinline__ i32x4 wide_words(const void *base) {
     const uint64_t b = reinterpret_cast<uint64_t>(base);
     return i32x4{__builtin_amdgcn_readfirstlane(int(uint32_t(b))),
@@ -536,72 +529,100 @@ __global__ __launch_bounds__(64 * WM * WN, OCC) void k_i8_tile(I8Args a, int til
 }
 
 // ---------------------------------------------------------------------------
-// Few-rows kernel: 16 * MB rows of x against 16 * NB weight rows per
-// workgroup, bound by the weight stream.
+// Rows kernel: 16 * MB rows of x against 16 * NB weight rows per workgroup,
+// for products too small to fill the device with tiles, down to one row,
+// where the weight stream is all there is.
 //
-// The eight waves split K: wave w takes the 128-byte units w, w + 8, ... of
-// every row, each as two v_mfma_i32_16x16x64_i8 per block pair, fragments
-// loaded straight into registers (lane: row lane % 16, 16 bytes lane / 16):
-// nothing of the weights is used twice, so LDS would only add a trip.  The
-// waves' int32 sums are added through LDS, exactly.
+// The four waves split K: wave w takes the 128-byte units w, w + 4, ... of
+// every row, each as two v_mfma_i32_16x16x64_i8 per pair of blocks, through a
+// ring of two units in LDS of its own: no wave waits for another before the
+// int32 sums are added, exactly, at the end.  The units come by DMA, eight
+// rows of 128 bytes an instruction.  (Fragments loaded straight into
+// registers touch 16 rows an instruction, which the address unit serves at
+// 16 B/clk per CU instead of 53: 16 x 18944 x 3584 17.5 us against 13.0,
+// 16 x 3584 x 18944 19.5 against 11.9.)  Rows of x that do not exist fetch
+// nothing.  Two units per wave keep three to five workgroups on a CU; four
+// units and eight waves, which leave one, were slower (18.7 us and 12.1).
+// LDS chunks are swizzled as in the tile kernel.
 // ---------------------------------------------------------------------------
-template <int MB, int NB, int DEPTH, typename O, bool GROUPED>
-__global__ __launch_bounds__(512) void k_i8_rows(I8Args a, int tiles_m, int tiles_n) {
-    constexpr int W = 8, BM = 16 * MB, BN = 16 * NB;
-    __shared__ __align__(16) int part[W][MB * NB][4][64];
+template <int MB, int NB, typename O, bool GROUPED>
+__global__ __launch_bounds__(256) void k_i8_rows(I8Args a, int tiles_n) {
+    constexpr int W = 4, NS = 2, BM = 16 * MB, BN = 16 * NB;
+    constexpr int D = 2 * (MB + NB), UNIT = D * 1024;      // DMA instructions and bytes of a unit
+    static_assert(NS * UNIT >= MB * NB * 1024, "the sums reuse the ring");
+    __shared__ __align__(1024) uint8_t S[W * NS * UNIT];
     const int tid = threadIdx.x, lane = tid & 63, wv = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int tn = blockIdx.x % tiles_n, tm = blockIdx.x / tiles_n;
     int e = 0, row0 = tm * BM, end = int(a.M);
     if (GROUPED && !find_group<BM>(a.offsets, a.E, int(a.M), tm, e, row0, end)) return;
-    const int n0 = tn * BN, K = int(a.K), N = int(a.N);
+    const int n0 = tn * BN, K = int(a.K), N = int(a.N), units = (K + 127) / 128;
     const bool gather = GROUPED && a.rows;
-    const __amdgpu_buffer_rsrc_t rx = wide_rsrc(a.x + (gather ? 0 : int64_t(row0) * a.ldx));
-    const __amdgpu_buffer_rsrc_t rw = wide_rsrc(a.w + (int64_t(e) * a.N + n0) * a.ldw);
-    const int kc = 16 * (lane >> 4);
-    uint32_t vx[MB], vw[NB];
+    const i32x4 rx = wide_words(a.x + (gather ? 0 : int64_t(row0) * a.ldx));
+    const i32x4 rw = wide_words(a.w + (int64_t(e) * a.N + n0) * a.ldw);
+    int ch[2];                                             // source chunk of even and odd instructions
 #pragma unroll
-    for (int j = 0; j < NB; j++) vw[j] = uint32_t(min(16 * j + (lane & 15), N - n0 - 1)) * uint32_t(a.ldw) + kc;
+    for (int p = 0; p < 2; p++) ch[p] = 16 * ((lane & 7) ^ ((p * 4 + (lane >> 4)) & 7));
+    uint32_t off[D];                                       // 2 NB instructions of the weights, then 2 MB of x
 #pragma unroll
-    for (int i = 0; i < MB; i++) {
-        const int r = min(16 * i + (lane & 15), end - row0 - 1);
-        vx[i] = (gather ? uint32_t(max(source_row<GROUPED>(a, row0 + r), 0)) : uint32_t(r)) * uint32_t(a.ldx) + kc;
+    for (int d = 0; d < D; d++) {
+        const int r = (d < 2 * NB ? d : d - 2 * NB) * 8 + (lane >> 3);
+        if (d < 2 * NB)
+            off[d] = uint32_t(min(r, N - n0 - 1)) * uint32_t(a.ldw) + ch[d & 1];
+        else {
+            const int src = row0 + r >= end ? -1 : gather ? source_row<GROUPED>(a, row0 + r) : r;
+            off[d] = src < 0 ? kNowhere : uint32_t(src) * uint32_t(a.ldx) + ch[d & 1];
+        }
     }
+    const uint32_t ring = lds_address(S) + wv * NS * UNIT;
+    auto load = [&](int u, int slot) {                     // past the last unit: fetches nothing
+        const int k0 = u * 128;
+        const bool in0 = k0 + ch[0] < K, in1 = k0 + ch[1] < K;
+#pragma unroll
+        for (int d = 0; d < D; d++)
+            dma16(d < 2 * NB ? rw : rx, ring + slot * UNIT + d * 1024, (d & 1 ? in1 : in0) ? off[d] : kNowhere, k0);
+    };
     i32x4 acc[MB][NB] = {};
-    const int units = (K + 127) / 128;
-    for (int u0 = wv; u0 < units; u0 += W * DEPTH) {
-        i32x4 fw[DEPTH][2][NB], fx[DEPTH][2][MB];
+    const uint8_t *mine = S + wv * NS * UNIT + (lane & 15) * 128;
+    int co[2];                                             // fragment: row lane % 16, 16 bytes lane / 16 of each half
 #pragma unroll
-        for (int d = 0; d < DEPTH; d++)
+    for (int p = 0; p < 2; p++) co[p] = 16 * ((4 * p + (lane >> 4)) ^ ((lane >> 1) & 7));
 #pragma unroll
-            for (int p = 0; p < 2; p++) {
-                const int k0 = (u0 + d * W) * 128 + 64 * p;
-                const bool in = k0 + kc < K;
+    for (int i = 0; i < NS; i++) load(wv + i * W, i);
+    int slot = 0;
+    for (int u = wv; u < units; u += W, slot ^= 1) {
+        asm volatile("s_waitcnt vmcnt(%0)" ::"n"((NS - 1) * D) : "memory");
+        const uint8_t *s = mine + slot * UNIT;
+        i32x4 fw[2][NB], fx[2][MB];
 #pragma unroll
-                for (int j = 0; j < NB; j++) fw[d][p][j] = load16(rw, in ? vw[j] : kNowhere, k0);
+        for (int p = 0; p < 2; p++) {
 #pragma unroll
-                for (int i = 0; i < MB; i++) fx[d][p][i] = load16(rx, in ? vx[i] : kNowhere, k0);
-            }
+            for (int j = 0; j < NB; j++) fw[p][j] = *reinterpret_cast<const i32x4 *>(s + j * 2048 + co[p]);
 #pragma unroll
-        for (int d = 0; d < DEPTH; d++)
+            for (int i = 0; i < MB; i++) fx[p][i] = *reinterpret_cast<const i32x4 *>(s + (NB + i) * 2048 + co[p]);
+        }
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); // the slot is in registers
+        load(u + NS * W, slot);
 #pragma unroll
-            for (int p = 0; p < 2; p++)
+        for (int p = 0; p < 2; p++)
 #pragma unroll
-                for (int i = 0; i < MB; i++)
+            for (int i = 0; i < MB; i++)
 #pragma unroll
-                    for (int j = 0; j < NB; j++)
-                        acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fw[d][p][j], fx[d][p][i], acc[i][j], 0, 0, 0);
+                for (int j = 0; j < NB; j++)
+                    acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fw[p][j], fx[p][i], acc[i][j], 0, 0, 0);
     }
+    wait_dma<0>();
+    int *part = reinterpret_cast<int *>(S);
 #pragma unroll
     for (int i = 0; i < MB; i++)
 #pragma unroll
         for (int j = 0; j < NB; j++)
-#pragma unroll
-            for (int r = 0; r < 4; r++) part[wv][i * NB + j][r][lane] = acc[i][j][r];
+            reinterpret_cast<i32x4 *>(part)[(wv * MB * NB + i * NB + j) * 64 + lane] = acc[i][j];
     __syncthreads();
     // register r of lane l: row (of x) l % 16, column 4 * (l / 16) + r
     const bool has_bias = a.bias != nullptr;
     O *out = static_cast<O *>(a.out);
-    for (int o = tid; o < BM * BN; o += 512) {
+#pragma unroll
+    for (int o = tid; o < BM * BN; o += 64 * W) {
         const int mr = o / BN, nr = o % BN, m = row0 + mr, n = n0 + nr;
         if (m >= end || n >= N) continue;
         const int src = source_row<GROUPED>(a, m);
@@ -609,8 +630,9 @@ __global__ __launch_bounds__(512) void k_i8_rows(I8Args a, int tiles_m, int tile
         const int l = (mr & 15) + 16 * ((nr & 15) >> 2), r = nr & 3, b = (mr >> 4) * NB + (nr >> 4);
         int sum = 0;
 #pragma unroll
-        for (int w = 0; w < W; w++) sum += part[w][b][r][l];
-        out[int64_t(m) * a.ldo + n] = scaled<O>(sum, a.xs[src], a.ws[int64_t(e) * a.N + n], has_bias ? a.bias[n] : 0.0f, has_bias);
+        for (int w = 0; w < W; w++) sum += part[((w * MB * NB + b) * 64 + l) * 4 + r];
+        out[int64_t(m) * a.ldo + n] =
+            scaled<O>(sum, a.xs[src], a.ws[int64_t(e) * a.N + n], has_bias ? a.bias[n] : 0.0f, has_bias);
     }
 }
 
@@ -647,9 +669,11 @@ static void launch_kernel(const I8Plan &p, const I8Args &a, hipStream_t stream) 
     case I8_TILE_128x256: k_i8_tile<128, 256, 2, 4, 3, 2, O, GROUPED><<<grid, 512, 0, stream>>>(a, tm, tn); break;
     case I8_TILE_128x128: k_i8_tile<128, 128, 2, 2, 2, 2, O, GROUPED><<<grid, 256, 0, stream>>>(a, tm, tn); break;
     case I8_TILE_64x128: k_i8_tile<64, 128, 1, 4, 2, 3, O, GROUPED><<<grid, 256, 0, stream>>>(a, tm, tn); break;
-    case I8_ROWS_16: k_i8_rows<1, 1, 4, O, GROUPED><<<grid, 512, 0, stream>>>(a, tm, tn); break;
-    case I8_ROWS_32: k_i8_rows<2, 1, 2, O, GROUPED><<<grid, 512, 0, stream>>>(a, tm, tn); break;
-    case I8_ROWS_64: k_i8_rows<4, 1, 2, O, GROUPED><<<grid, 512, 0, stream>>>(a, tm, tn); break;
+    case I8_ROWS_16x16: k_i8_rows<1, 1, O, GROUPED><<<grid, 256, 0, stream>>>(a, tn); break;
+    case I8_ROWS_16x32: k_i8_rows<1, 2, O, GROUPED><<<grid, 256, 0, stream>>>(a, tn); break;
+    case I8_ROWS_32x32: k_i8_rows<2, 2, O, GROUPED><<<grid, 256, 0, stream>>>(a, tn); break;
+    case I8_ROWS_32x64: k_i8_rows<2, 4, O, GROUPED><<<grid, 256, 0, stream>>>(a, tn); break;
+    case I8_ROWS_64x64: k_i8_rows<4, 4, O, GROUPED><<<grid, 256, 0, stream>>>(a, tn); break;
     }
 }
 

@@ -48,10 +48,12 @@ inline const char *check_gemm_i8(int64_t M, int64_t N, int64_t K, int64_t ldx, i
     return nullptr;
 }
 
-// Kernels of the products: tiles of BM x BN outputs, and the few-rows kernel
-// of 16, 32 or 64 rows of x against 16 weight rows.
+// Kernels of the products: the tile kernel (tiles of BM x BN outputs), and
+// the rows kernel (workgroups of BM x BN outputs that split K over waves).
 enum I8Kernel : int {
-    I8_TILE_256x256, I8_TILE_128x256, I8_TILE_128x128, I8_TILE_64x128, I8_ROWS_16, I8_ROWS_32, I8_ROWS_64, I8_KERNELS
+    I8_TILE_256x256, I8_TILE_128x256, I8_TILE_128x128, I8_TILE_64x128,
+    I8_ROWS_16x16, I8_ROWS_16x32, I8_ROWS_32x32, I8_ROWS_32x64, I8_ROWS_64x64,
+    I8_KERNELS
 };
 struct I8KernelInfo {
     const char *name;
@@ -62,9 +64,9 @@ struct I8KernelInfo {
     double step_us, fixed_us;
 };
 constexpr I8KernelInfo kI8Kernels[I8_KERNELS] = {
-    {"tile", 256, 256, 512, 1, 1.55, 6.0}, {"tile", 128, 256, 512, 1, 0.87, 5.5}, {"tile", 128, 128, 256, 2, 0.51, 3.0},
-    {"tile", 64, 128, 256, 2, 0.30, 2.0},  {"rows", 16, 16, 512, 0, 0.0, 0.0},    {"rows", 32, 16, 512, 0, 0.0, 0.0},
-    {"rows", 64, 16, 512, 0, 0.0, 0.0},
+    {"tile", 256, 256, 512, 1, 1.45, 9.5}, {"tile", 128, 256, 512, 1, 0.87, 5.5}, {"tile", 128, 128, 256, 2, 0.51, 3.0},
+    {"tile", 64, 128, 256, 2, 0.30, 2.0},  {"rows", 16, 16, 256, 0, 0.0, 0.0},    {"rows", 16, 32, 256, 0, 0.0, 0.0},
+    {"rows", 32, 32, 256, 0, 0.0, 0.0},    {"rows", 32, 64, 256, 0, 0.0, 0.0},    {"rows", 64, 64, 256, 0, 0.0, 0.0},
 };
 
 struct I8Plan {
@@ -88,20 +90,31 @@ inline bool make_plan_i8(int64_t M, int64_t N, int64_t K, int experts, int cu_co
         std::snprintf(why, why_len, "device reports no compute units");
         return false;
     }
-    // rows that share a weight matrix, on average
-    const int64_t per = experts ? (M + experts - 1) / experts : M;
-    if (per <= 64) {
-        p->kernel = per <= 16 ? I8_ROWS_16 : per <= 32 ? I8_ROWS_32 : I8_ROWS_64;
+    // rows that share a weight matrix, on average, and the tiles to expect: a
+    // group's last row tile is half full on average
+    const int64_t per = experts ? (M + experts - 1) / experts : M, groups = experts ? (M < experts ? M : experts) : 0;
+    auto tiles_of = [&](int v) {
+        const I8KernelInfo &k = kI8Kernels[v];
+        const int64_t row_tiles = experts ? M / k.tile_m + (groups + 1) / 2 : (M + k.tile_m - 1) / k.tile_m;
+        return row_tiles * ((N + k.tile_n - 1) / k.tile_n);
+    };
+    // The rows kernel where a weight matrix meets few rows (16 x 18944 x 3584
+    // 13.0 us against 14.5 in 64 x 128 tiles, 4 rows for each of 128 experts
+    // 73.4 against 74.3, 16 rows 101 against 78) and where the smallest tiles
+    // would leave half the CUs without one (128 x 3584 x 18944, 56 tiles: 22.3
+    // against 48.1; 256 x 3584 x 3584, 112 tiles: 11.2 against 12.9).
+    if (per <= (experts ? 4 : 16) || tiles_of(I8_TILE_64x128) * 2 < cu_count) {
+        // the largest workgroup that still makes about one per CU: 64 x 3584 x
+        // 18944 as 16 x 32 22.9, 32 x 32 16.2, 32 x 64 (112 of them) 22.3
+        p->kernel = I8_ROWS_16x16;
+        for (int v = I8_ROWS_16x32; v <= I8_ROWS_64x64; v++)
+            if ((kI8Kernels[v].tile_m == 16 || per > kI8Kernels[v].tile_m / 2) && tiles_of(v) * 5 >= cu_count * 4) p->kernel = v;
     } else {
         const int64_t steps = (K + 127) / 128;
         double best = 0;
         for (int v = I8_TILE_256x256; v <= I8_TILE_64x128; v++) {
             const I8KernelInfo &k = kI8Kernels[v];
-            // a group's last row tile is half full on average
-            const int64_t groups = experts ? (M < experts ? M : experts) : 0;
-            const int64_t row_tiles = experts ? M / k.tile_m + (groups + 1) / 2 : (M + k.tile_m - 1) / k.tile_m;
-            const int64_t tiles = row_tiles * ((N + k.tile_n - 1) / k.tile_n);
-            const double us = double((tiles + cu_count - 1) / cu_count) * (double(steps) * k.step_us + k.fixed_us);
+            const double us = double((tiles_of(v) + cu_count - 1) / cu_count) * (double(steps) * k.step_us + k.fixed_us);
             if (v == I8_TILE_256x256 || us < best) {
                 best = us;
                 p->kernel = v;
