@@ -363,7 +363,9 @@ def debug_block_dots(fmt, xq, w, M, N, K, dots=None, stream=None):
 # row; products of them in fp32, bf16 or fp16.  These calls take their sizes
 # from the tensors, accept rows with a pitch (a slice of columns) wherever
 # the library does, and run on the GPU that holds the tensors, whichever
-# device is current: on `stream`, or else on that GPU's current stream.
+# device is current: on `stream`, or else on that GPU's current stream.  With
+# a `stream`, results are allocated on it, and the tensors handed in are kept
+# from reuse until its work is done (record_stream).
 # ---------------------------------------------------------------------------
 I8_MAX_K = 131056
 
@@ -373,8 +375,7 @@ def _pad16(K) -> int:
 
 
 def _type_code(dtype) -> int:
-    import torch
-    code = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}.get(dtype)
+    code = _c().codes.get(dtype)
     if code is None:
         raise ValueError(f"expected torch.float32, torch.bfloat16 or torch.float16, got {dtype}")
     return code
@@ -384,13 +385,15 @@ def _matrix(t, what, dtype=None, rows=None, cols=None, dev=None):
     """Row pitch of the matrix ``t`` in elements; its columns must be adjacent."""
     if t.dim() != 2:
         raise ValueError(f"{what}: expected a matrix, got shape {tuple(t.shape)}")
-    if dtype is not None and t.dtype != dtype:
+    if dtype is not None and t.dtype is not dtype:
         raise ValueError(f"{what}: expected {dtype}, got {t.dtype}")
     r, c = t.shape
     if (rows is not None and r != rows) or (cols is not None and c != cols):
         raise ValueError(f"{what}: expected shape ({rows if rows is not None else r}, "
                          f"{cols if cols is not None else c}), got {tuple(t.shape)}")
     _on(t, what, dev)
+    if t.is_contiguous():
+        return c
     sr, sc = t.stride()
     if c > 1 and sc != 1:
         raise ValueError(f"{what}: the columns of a row must be adjacent (stride 1), got strides {t.stride()}")
@@ -400,12 +403,12 @@ def _matrix(t, what, dtype=None, rows=None, cols=None, dev=None):
 
 
 def _vector(t, what, dtype, n, dev):
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise ValueError(f"{what}: expected {dtype}, got {t.dtype}")
-    if t.dim() != 1 or t.shape[0] != n:
+    if t.shape != (n,):
         raise ValueError(f"{what}: expected shape ({n},), got {tuple(t.shape)}")
     _on(t, what, dev)
-    if n > 1 and t.stride(0) != 1:
+    if not t.is_contiguous():
         raise ValueError(f"{what}: must be contiguous")
     return t.data_ptr()
 
@@ -417,30 +420,72 @@ def _on(t, what, dev):
         raise ValueError(f"{what} is on {t.device}, the other tensors on {dev}")
 
 
-def _launch(fn, name, dev, stream, *args):
-    """Call ``fn`` on ``dev`` (made current for the call) and its stream."""
-    import torch
-    if stream is not None and stream.device != dev:
+class _Calls:
+    """What a call of the operators below needs of torch and the library,
+    looked up once: a product of one token takes less time on the GPU than
+    the lookups would on the host."""
+
+    def __init__(self):
+        import torch
+        self.empty, self.device, self.stream = torch.empty, torch.cuda.device, torch.cuda.stream
+        self.i8, self.f32, self.i32 = torch.int8, torch.float32, torch.int32
+        self.codes = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+        self.current_device, self.raw_stream = torch.cuda.current_device, torch._C._cuda_getCurrentRawStream
+        L = lib()
+        self.quantize, self.silu_mul = L.mmq_quantize_i8, L.mmq_silu_mul_quantize_i8
+        self.gemm, self.grouped = L.mmq_gemm_i8, L.mmq_grouped_gemm_i8
+
+
+_calls = None
+
+
+def _c() -> _Calls:
+    global _calls
+    if _calls is None:
+        _calls = _Calls()
+    return _calls
+
+
+def _empty(shape, dtype, dev, stream):
+    c = _c()
+    if stream is None:
+        return c.empty(shape, dtype=dtype, device=dev)
+    with c.stream(stream):
+        return c.empty(shape, dtype=dtype, device=dev)
+
+
+def _launch(fn, name, dev, stream, tensors, *args):
+    """Call ``fn`` on ``dev`` (made current for the call) and its stream;
+    ``tensors``: what it reads and writes."""
+    c = _c()
+    if stream is None:
+        s = c.raw_stream(dev.index)
+    elif stream.device == dev:
+        s = stream.cuda_stream
+        if s != c.raw_stream(dev.index):
+            for t in tensors:
+                if t is not None:
+                    t.record_stream(stream)
+    else:
         raise ValueError(f"the stream is on {stream.device}, the tensors on {dev}")
-    s = torch._C._cuda_getCurrentRawStream(dev.index) if stream is None else stream.cuda_stream
-    if torch.cuda.current_device() == dev.index:
+    if c.current_device() == dev.index:
         rc = fn(*args, s)
     else:
-        with torch.cuda.device(dev):
+        with c.device(dev):
             rc = fn(*args, s)
     if rc != 1:
         raise MMQError(f"{name}: {last_error()}")
 
 
-def _codes_out(q, scale, M, K, dev):
-    import torch
+def _codes_out(q, scale, M, K, dev, stream):
+    c = _c()
     Kp = _pad16(K)
     if q is None:
-        q = torch.empty((M, Kp), dtype=torch.int8, device=dev)
-    ldq = _matrix(q, "q", torch.int8, M, Kp, dev)
+        q = _empty((M, Kp), c.i8, dev, stream)
+    ldq = _matrix(q, "q", c.i8, M, Kp, dev)
     if scale is None:
-        scale = torch.empty((M,), dtype=torch.float32, device=dev)
-    return q, ldq, scale, _vector(scale, "scale", torch.float32, M, dev)
+        scale = _empty((M,), c.f32, dev, stream)
+    return q, ldq, scale, _vector(scale, "scale", c.f32, M, dev)
 
 
 def quantize_i8(x, q=None, scale=None, stream=None):
@@ -451,8 +496,9 @@ def quantize_i8(x, q=None, scale=None, stream=None):
     code = _type_code(x.dtype)
     ldx = _matrix(x, "x")
     M, K = x.shape
-    q, ldq, scale, sp = _codes_out(q, scale, M, K, dev)
-    _launch(lib().mmq_quantize_i8, "mmq_quantize_i8", dev, stream, code, x.data_ptr(), ldx, q.data_ptr(), ldq, sp, M, K)
+    q, ldq, scale, sp = _codes_out(q, scale, M, K, dev, stream)
+    _launch(_c().quantize, "mmq_quantize_i8", dev, stream, (x, q, scale), code, x.data_ptr(), ldx, q.data_ptr(), ldq,
+            sp, M, K)
     return q, scale
 
 
@@ -465,18 +511,18 @@ def silu_mul_quantize_i8(gate, up, q=None, scale=None, stream=None):
     M, K = gate.shape
     if _matrix(up, "up", gate.dtype, M, K, dev) != ld:
         raise ValueError(f"gate and up must have the same row pitch, got strides {gate.stride()} and {up.stride()}")
-    q, ldq, scale, sp = _codes_out(q, scale, M, K, dev)
-    _launch(lib().mmq_silu_mul_quantize_i8, "mmq_silu_mul_quantize_i8", dev, stream, code, gate.data_ptr(),
+    q, ldq, scale, sp = _codes_out(q, scale, M, K, dev, stream)
+    _launch(_c().silu_mul, "mmq_silu_mul_quantize_i8", dev, stream, (gate, up, q, scale), code, gate.data_ptr(),
             up.data_ptr(), ld, q.data_ptr(), ldq, sp, M, K)
     return q, scale
 
 
-def _product_out(out, dtype, M, N, dev):
-    import torch
+def _product_out(out, dtype, M, N, dev, stream):
+    c = _c()
     if out is None:
-        dtype = torch.float32 if dtype is None else dtype
+        dtype = c.f32 if dtype is None else dtype
         code = _type_code(dtype)
-        return torch.empty((M, N), dtype=dtype, device=dev), code, N
+        return _empty((M, N), dtype, dev, stream), code, N
     if dtype is not None and out.dtype != dtype:
         raise ValueError(f"out: expected {dtype}, got {out.dtype}")
     return out, _type_code(out.dtype), _matrix(out, "out", None, M, N, dev)
@@ -486,18 +532,18 @@ def gemm_i8(xq, xs, wq, ws, bias=None, dtype=None, out=None, stream=None):
     """Codes [M, K] x codes [N, K] with fp32 scales per token (xs [M]) and per
     channel (ws [N]), plus an optional fp32 bias [N] -> [M, N] of ``dtype``
     (float32 by default).  The integer sum is exact."""
-    import torch
+    c = _c()
     dev = xq.device
-    ldx = _matrix(xq, "xq", torch.int8)
+    ldx = _matrix(xq, "xq", c.i8)
     M, K = xq.shape
-    ldw = _matrix(wq, "wq", torch.int8, None, K, dev)
+    ldw = _matrix(wq, "wq", c.i8, None, K, dev)
     N = wq.shape[0]
-    xp = _vector(xs, "xs", torch.float32, M, dev)
-    wp = _vector(ws, "ws", torch.float32, N, dev)
-    bp = None if bias is None else _vector(bias, "bias", torch.float32, N, dev)
-    out, code, ldo = _product_out(out, dtype, M, N, dev)
-    _launch(lib().mmq_gemm_i8, "mmq_gemm_i8", dev, stream, code, xq.data_ptr(), ldx, xp, wq.data_ptr(), ldw, wp, bp,
-            out.data_ptr(), ldo, M, N, K)
+    xp = _vector(xs, "xs", c.f32, M, dev)
+    wp = _vector(ws, "ws", c.f32, N, dev)
+    bp = None if bias is None else _vector(bias, "bias", c.f32, N, dev)
+    out, code, ldo = _product_out(out, dtype, M, N, dev, stream)
+    _launch(c.gemm, "mmq_gemm_i8", dev, stream, (xq, xs, wq, ws, bias, out), code, xq.data_ptr(), ldx, xp, wq.data_ptr(),
+            ldw, wp, bp, out.data_ptr(), ldo, M, N, K)
     return out
 
 
@@ -508,11 +554,11 @@ def grouped_gemm_i8(xq, xs, wq, ws, offsets, rows=None, dtype=None, out=None, st
     [E + 1] and ``rows`` int32 [R] stay on the device.  Rows outside every
     group, and rows whose index is out of range, are left as they were (in a
     fresh ``out``: undefined)."""
-    import torch
+    c = _c()
     dev = xq.device
-    ldx = _matrix(xq, "xq", torch.int8)
+    ldx = _matrix(xq, "xq", c.i8)
     T, K = xq.shape
-    if wq.dim() != 3 or wq.dtype != torch.int8:
+    if wq.dim() != 3 or wq.dtype != c.i8:
         raise ValueError(f"wq: expected int8 [experts, N, K], got {wq.dtype} {tuple(wq.shape)}")
     E, N, Kw = wq.shape
     if Kw != K:
@@ -520,18 +566,18 @@ def grouped_gemm_i8(xq, xs, wq, ws, offsets, rows=None, dtype=None, out=None, st
     _on(wq, "wq", dev)
     if not wq.is_contiguous():
         raise ValueError("wq must be contiguous")
-    if tuple(ws.shape) != (E, N) or ws.dtype != torch.float32 or not ws.is_contiguous():
+    if tuple(ws.shape) != (E, N) or ws.dtype != c.f32 or not ws.is_contiguous():
         raise ValueError(f"ws: expected contiguous float32 ({E}, {N}), got {ws.dtype} {tuple(ws.shape)}")
     _on(ws, "ws", dev)
-    xp = _vector(xs, "xs", torch.float32, T, dev)
-    op = _vector(offsets, "offsets", torch.int32, E + 1, dev)
+    xp = _vector(xs, "xs", c.f32, T, dev)
+    op = _vector(offsets, "offsets", c.i32, E + 1, dev)
     R, rp = T, None
     if rows is not None:
         R = rows.numel()
-        rp = _vector(rows, "rows", torch.int32, R, dev)
-    out, code, ldo = _product_out(out, dtype, R, N, dev)
-    _launch(lib().mmq_grouped_gemm_i8, "mmq_grouped_gemm_i8", dev, stream, code, xq.data_ptr(), ldx, xp, T, rp, op, E,
-            wq.data_ptr(), K, ws.data_ptr(), out.data_ptr(), ldo, R, N, K)
+        rp = _vector(rows, "rows", c.i32, R, dev)
+    out, code, ldo = _product_out(out, dtype, R, N, dev, stream)
+    _launch(c.grouped, "mmq_grouped_gemm_i8", dev, stream, (xq, xs, wq, ws, offsets, rows, out), code, xq.data_ptr(), ldx,
+            xp, T, rp, op, E, wq.data_ptr(), K, ws.data_ptr(), out.data_ptr(), ldo, R, N, K)
     return out
 
 

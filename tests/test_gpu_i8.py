@@ -423,6 +423,26 @@ def test_two_streams_at_once():
         assert all(torch.equal(o, want[i]) for o in outs[i])
 
 
+def test_inputs_of_a_call_on_another_stream_are_kept_until_it_ran():
+    """The call waits on its stream behind a long product; its inputs are
+    dropped at once and their memory is written by the current stream."""
+    M, N, K = 300, 500, 4096
+    wq, ws = codes(N, K, 1), scales(N, 2)
+    side = torch.cuda.Stream()
+    big = torch.randn((8192, 8192), device=DEV)
+    xq, xs = codes(M, K, 3), scales(M, 4)
+    want = mmq.gemm_i8(xq, xs, wq, ws)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        for _ in range(4):
+            big @ big
+    out = mmq.gemm_i8(xq, xs, wq, ws, stream=side)
+    del xq, xs
+    junk = [torch.full((M, K), 1, dtype=torch.int8, device=DEV) for _ in range(4)] + [torch.zeros(M, device=DEV) for _ in range(4)]
+    torch.cuda.synchronize()
+    assert torch.equal(out, want) and len(junk) == 8
+
+
 def test_no_rows():
     z = torch.empty((0, 64), dtype=BF16, device=DEV)
     q, s = mmq.quantize_i8(z)
