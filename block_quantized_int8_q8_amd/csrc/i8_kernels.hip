@@ -99,10 +99,10 @@ __device__ __forceinline__ void silu_mul(float (&v)[kChunk], const float (&u)[kC
 template <typename T, bool SILU, int THREADS, int CH>
 __global__ __launch_bounds__(THREADS < 256 ? 256 : THREADS) void k_quantize_i8(
     const T *__restrict__ x, const T *__restrict__ up, int64_t ldx, int8_t *__restrict__ q, int64_t ldq,
-    float *__restrict__ scale, int M, int K) {
+    float *__restrict__ scale, int64_t first, int M, int K) {
     constexpr int ROWS = THREADS < 256 ? 256 / THREADS : 1;
     const int tid = threadIdx.x % THREADS, chunks = (K + 15) / 16 * 2;   // codes are padded to a multiple of 16
-    const int64_t row = int64_t(blockIdx.x) * ROWS + threadIdx.x / THREADS;
+    const int64_t row = first + int64_t(blockIdx.x) * ROWS + threadIdx.x / THREADS;
     if (ROWS > 1 && row >= M) return;                                    // whole waves: a row's threads are one
     const T *xr = x + row * ldx, *ur = SILU ? up + row * ldx : nullptr;
     // the largest magnitude as integer bits: NaN > infinity > any finite
@@ -176,27 +176,43 @@ __global__ __launch_bounds__(THREADS < 256 ? 256 : THREADS) void k_quantize_i8(
 // GEMM
 // ---------------------------------------------------------------------------
 
+// Inclusive scans over the lanes of a wave.
+__device__ __forceinline__ int scan_sum(int v) {
+    const int lane = threadIdx.x & 63;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+        const int u = __shfl_up(v, o);
+        if (lane >= o) v += u;
+    }
+    return v;
+}
+__device__ __forceinline__ int scan_max(int v) {
+    const int lane = threadIdx.x & 63;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+        const int u = __shfl_up(v, o);
+        if (lane >= o) v = max(v, u);
+    }
+    return v;
+}
+
 // The group that tile `tile` of a grouped launch belongs to: its expert and
-// its rows [row, end).  Expert e has ceil(len_e / TM) tiles; a wave scans the
-// experts 64 at a time.  False past the last tile.  Bounds are clamped to
-// [0, M], so no offsets make the kernel leave its buffers.
+// its rows [row, end).  A wave scans the experts 64 at a time; false past the
+// last tile.  Offsets are clamped to [0, M], and a group starts no earlier
+// than any before it ended, so whatever the offsets say, tiles lie within the
+// buffers and there are at most M / TM + E of them.
 template <int TM>
 __device__ __forceinline__ bool find_group(const int32_t *__restrict__ offsets, int E, int M, int tile, int &e,
                                            int &row, int &end) {
     const int lane = threadIdx.x & 63;
-    int before = 0;
+    int before = 0, seen = min(max(offsets[0], 0), M);
     for (int e0 = 0; e0 < E; e0 += 64) {
-        int b = 0, t = 0;
-        if (e0 + lane < E) {
-            b = min(max(offsets[e0 + lane], 0), M);
-            t = min(max(offsets[e0 + lane + 1], 0), M);
-        }
-        const int n = t > b ? (t - b + TM - 1) / TM : 0;
-        int upto = n;
-        for (int o = 1; o < 64; o <<= 1) {
-            const int v = __shfl_up(upto, o);
-            if (lane >= o) upto += v;
-        }
+        int t = 0;
+        if (e0 + lane < E) t = min(max(offsets[e0 + lane + 1], 0), M);
+        t = max(scan_max(t), seen);
+        int b = __shfl_up(t, 1);
+        if (lane == 0) b = seen;
+        const int n = (t - b + TM - 1) / TM, upto = scan_sum(n);
         const unsigned long long hit = __ballot(before + upto > tile);
         if (hit) {
             const int l = __builtin_ctzll(hit);
@@ -206,6 +222,7 @@ __device__ __forceinline__ bool find_group(const int32_t *__restrict__ offsets, 
             return true;
         }
         before += __builtin_amdgcn_readlane(upto, 63);
+        seen = __builtin_amdgcn_readlane(t, 63);
     }
     return false;
 }
@@ -302,8 +319,13 @@ __device__ __forceinline__ void wait_dma() {
 // Such a buffer's descriptor, in scalar registers.
 __device__ __forceinline__ i32x4 wide_words(const void *base) {
     const uint64_t b = reinterpret_cast<uint64_t>(base);
-    return i32x4{__builtin_amdgcn_readfirstlane(int(uint32_t(b))),
-                 __builtin_amdgcn_readfirstlane(int(uint32_t(b >> 32) & 0xffffu)), int(kBufBytes), 0x00020000};
+    i32x4 r{__builtin_amdgcn_readfirstlane(int(uint32_t(b))),
+            __builtin_amdgcn_readfirstlane(int(uint32_t(b >> 32) & 0xffffu)), int(kBufBytes), 0x00020000};
+    // a memory instruction reads a scalar register at least five wait states
+    // after a vector instruction wrote it; the compiler does not see that the
+    // assembly below is one
+    asm volatile("s_nop 4" : "+s"(r));
+    return r;
 }
 __device__ __forceinline__ uint32_t lds_address(const void *p) {
     return uint32_t(reinterpret_cast<uintptr_t>((lds_void *)p));
@@ -318,39 +340,42 @@ __device__ __forceinline__ void unrolled(F f) {
 }
 template <int V> using constant = std::integral_constant<int, V>;
 
-// Row tiles of every expert: start[e] becomes the first tile of expert e, the
-// sum is returned.  Bounds are clamped to [0, M]: no offsets make the kernel
-// leave its buffers.
+// Row tiles of every expert, by the rule of find_group: start[e] becomes the
+// first tile of expert e, the sum is returned.
 template <int TM, int THREADS>
 __device__ __forceinline__ int scan_groups(const I8Args &a, int *start, int *part) {
     const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6, M = int(a.M);
-    int carry = 0;
+    int tiles = 0, seen = min(max(a.offsets[0], 0), M);
     for (int e0 = 0; e0 < a.E; e0 += THREADS) {
         const int e = e0 + tid;
-        int n = 0;
-        if (e < a.E) {
-            const int b = min(max(a.offsets[e], 0), M), t = min(max(a.offsets[e + 1], 0), M);
-            n = t > b ? (t - b + TM - 1) / TM : 0;
-        }
-        int upto = n;
+        int t = scan_max(e < a.E ? min(max(a.offsets[e + 1], 0), M) : 0);
+        if (lane == 63) part[wv] = t;
+        __syncthreads();
+        int last = seen, most = seen;                              // of the waves before this one, and of all
 #pragma unroll
-        for (int o = 1; o < 64; o <<= 1) {
-            const int v = __shfl_up(upto, o);
-            if (lane >= o) upto += v;
+        for (int w = 0; w < THREADS / 64; w++) {
+            if (w < wv) last = max(last, part[w]);
+            most = max(most, part[w]);
         }
+        t = max(t, last);
+        int b = __shfl_up(t, 1);
+        if (lane == 0) b = last;
+        const int n = (t - b + TM - 1) / TM, upto = scan_sum(n);
+        __syncthreads();
         if (lane == 63) part[wv] = upto;
         __syncthreads();
-        int before = carry, sum = 0;
+        int before = tiles, sum = 0;
 #pragma unroll
         for (int w = 0; w < THREADS / 64; w++) {
             if (w < wv) before += part[w];
             sum += part[w];
         }
         if (e < a.E) start[e] = before + upto - n;
-        carry += sum;
+        tiles += sum;
+        seen = most;
         __syncthreads();
     }
-    return __builtin_amdgcn_readfirstlane(carry);
+    return __builtin_amdgcn_readfirstlane(tiles);
 }
 // The expert of row tile `tile`: the last e with start[e] <= tile (of equal
 // starts only the last has tiles).  64-way search by one wave.
@@ -414,7 +439,7 @@ __global__ __launch_bounds__(64 * WM * WN, OCC) void k_i8_tile(I8Args a, int til
         if (GROUPED) {
             typedef const __attribute__((address_space(4))) int *scalar_ints;
             const scalar_ints off = (scalar_ints)a.offsets;
-            e = group_of(start, a.E, tm);
+            e = group_of(start, a.E, tm);          // (where offsets decrease, off[e] may lie before the group: still a row)
             row0 = min(max(off[e], 0), end) + (tm - __builtin_amdgcn_readfirstlane(start[e])) * BM;
             end = min(max(off[e + 1], 0), end);
         }
@@ -740,13 +765,19 @@ static hipError_t launch_rows(const void *x, const void *up, int64_t ldx, void *
     const T *xx = static_cast<const T *>(x), *uu = static_cast<const T *>(up);
     int8_t *qq = static_cast<int8_t *>(q);
     const int m = int(M), k = int(K);
-    // threads per row: a wave up to 2048 values, else as few as hold the row
-    if (K <= 64 * 4 * kChunk)
-        k_quantize_i8<T, SILU, 64, 4><<<dim3(unsigned((M + 3) / 4)), 256, 0, stream>>>(xx, uu, ldx, qq, ldq, scale, m, k);
-    else if (K <= 256 * 4 * kChunk)
-        k_quantize_i8<T, SILU, 256, 4><<<dim3(unsigned(M)), 256, 0, stream>>>(xx, uu, ldx, qq, ldq, scale, m, k);
-    else
-        k_quantize_i8<T, SILU, 1024, 3><<<dim3(unsigned(M)), 1024, 0, stream>>>(xx, uu, ldx, qq, ldq, scale, m, k);
+    // a launch holds fewer than 2^32 threads: at most kSlice rows each
+    constexpr int64_t kSlice = int64_t(1) << 21;
+    for (int64_t first = 0; first < M; first += kSlice) {
+        const unsigned n = unsigned(M - first < kSlice ? M - first : kSlice);
+        // threads per row: a wave up to 2048 values, else as many as hold the
+        // row in three or four chunks
+        if (K <= 64 * 4 * kChunk)
+            k_quantize_i8<T, SILU, 64, 4><<<dim3((n + 3) / 4), 256, 0, stream>>>(xx, uu, ldx, qq, ldq, scale, first, m, k);
+        else if (K <= 256 * 4 * kChunk)
+            k_quantize_i8<T, SILU, 256, 4><<<dim3(n), 256, 0, stream>>>(xx, uu, ldx, qq, ldq, scale, first, m, k);
+        else
+            k_quantize_i8<T, SILU, 1024, 3><<<dim3(n), 1024, 0, stream>>>(xx, uu, ldx, qq, ldq, scale, first, m, k);
+    }
     return hipGetLastError();
 }
 

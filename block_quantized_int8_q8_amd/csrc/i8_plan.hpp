@@ -127,13 +127,22 @@ inline bool make_plan_i8(int64_t M, int64_t N, int64_t K, int experts, int cu_co
     p->threads = k.threads;
     p->tiles_m = i8_row_tiles(M, experts, p->tile_m);
     p->tiles_n = (N + p->tile_n - 1) / p->tile_n;
-    if (p->tiles_m * p->tiles_n > INT32_MAX) {
+    p->workgroups = p->tiles_m * p->tiles_n;
+    if (p->workgroups > INT32_MAX) {
         std::snprintf(why, why_len, "%lld x %lld output tiles exceed the grid's 2^31 - 1", (long long)p->tiles_m,
                       (long long)p->tiles_n);
         return false;
     }
-    p->workgroups = p->tiles_m * p->tiles_n;
     if (k.per_cu && p->workgroups > int64_t(cu_count) * k.per_cu) p->workgroups = int64_t(cu_count) * k.per_cu;
+    if (p->workgroups * p->threads > UINT32_MAX) {
+        std::snprintf(why, why_len, "%lld output tiles of %d threads exceed a launch's 2^32 - 1 threads",
+                      (long long)p->workgroups, p->threads);
+        return false;
+    }
+    if (M > INT32_MAX - 512 || N > INT32_MAX - 512) {
+        std::snprintf(why, why_len, "the last output tile would pass 2^31 rows or columns");
+        return false;
+    }
     return true;
 }
 

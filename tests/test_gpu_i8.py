@@ -141,6 +141,33 @@ def test_gemm_beyond_32_bit_offsets():
     assert bool((out[:-300] == 0).all())
 
 
+def kernel_of(M, N, K, E=0):
+    ok, desc = mmq.plan_i8(M, N, K, E, torch.cuda.get_device_properties(0).multi_processor_count)
+    assert ok, desc
+    return desc.split(" threads")[0]
+
+
+# last k-steps of every length behind a long K (a step's offset then passes
+# the distance by which "nowhere" lies past a buffer's end), with the kernel
+# that runs each
+TAILS = [(300, 4000, 3600), (600, 1500, 2064), (700, 2100, 2096), (900, 3000, 4112), (1500, 2500, 3264), (2000, 3000, 2160),
+         (2500, 4000, 3504), (4000, 4100, 2064), (5000, 9000, 2128), (40, 600, 5008), (100, 2000, 4144), (200, 2000, 2192)]
+
+
+def test_gemm_long_k_tails_on_every_kernel():
+    seen = set()
+    for M, N, K in TAILS:
+        seen.add(kernel_of(M, N, K))
+        xq, wq, xs, ws = codes(M, K, M), codes(N, K, N), scales(M, 2), scales(N, 3)
+        out = mmq.gemm_i8(xq, xs, wq, ws)
+        acc = torch.matmul(xq.double(), wq.double().t())          # integers below 2^53: exact on the GPU as well
+        assert torch.equal(out, acc.float() * xs[:, None] * ws), (M, N, K)
+    for tile in ("256x256", "128x256", "128x128", "64x128"):
+        assert f"kernel=tile tile={tile}" in seen, seen
+    for tile in ("32x32", "32x64", "64x64"):
+        assert f"kernel=rows tile={tile}" in seen, seen
+
+
 # ---------------------------------------------------------------------------
 # grouped products
 # ---------------------------------------------------------------------------
@@ -192,6 +219,54 @@ def test_grouped(name, lengths, first, behind, gather, N, K):
     out = torch.full((R, N), -5.0, dtype=dtype, device=DEV)
     mmq.grouped_gemm_i8(xq, xs, wq, ws, off.to(DEV), rows=None if rows is None else rows.to(DEV), out=out)
     check_grouped(out, xq, xs, wq, ws, off, rows, dtype, -5.0)
+
+
+# (lengths, first, behind, N, K): groups whose sizes and number make the planner take tiles
+TILED = [([700, 0, 300, 1, 0, 900, 130, 64], 3, 9, 2100, 208), ([1] * 200 + [4000] + [0] * 50 + [257], 0, 40, 1030, 400),
+         ([(i * 37) % 23 for i in range(2048)], 5, 0, 130, 80), ([0] * 1024 + [9000] + [0] * 1000 + [77], 0, 0, 520, 2064),
+         ([128] * 64, 0, 0, 1536, 512), ([5000], 0, 3, 4000, 96), ([3000, 5000, 2, 4000], 0, 0, 5000, 144),
+         ([600 + 40 * i for i in range(17)], 0, 0, 2048, 160)]
+
+
+@pytest.mark.parametrize("gather", [False, True], ids=["inplace", "gather"])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_grouped_tiles(gather, dtype):
+    seen = set()
+    for lengths, first, behind, N, K in TILED:
+        E, R = len(lengths), first + sum(lengths) + behind
+        seen.add(kernel_of(R, N, K, E))
+        T = R // 5 if gather else R
+        off = offsets_of(lengths, first)
+        xq, xs, wq, ws = codes(T, K, R), scales(T, 1), codes(E * N, K, E).view(E, N, K), scales(E * N, 2).view(E, N)
+        rows = torch.randint(0, T, (R,), generator=gen(R), dtype=torch.int32) if gather else None
+        if gather:
+            rows[first + 1], rows[R // 2] = -7, T
+        out = torch.full((R, N), -5.0, dtype=dtype, device=DEV)
+        mmq.grouped_gemm_i8(xq, xs, wq, ws, off.to(DEV), rows=None if rows is None else rows.to(DEV), out=out)
+        src = torch.arange(R, device=DEV) if rows is None else rows.to(DEV).long()
+        want = torch.full((R, N), -5.0, dtype=dtype, device=DEV)
+        for e, (a, b) in enumerate(zip(off.tolist(), off.tolist()[1:])):
+            if b > a:
+                t = src[a:b].clamp(0, T - 1)
+                y = torch.matmul(xq[t].double(), wq[e].double().t()).float() * xs[t][:, None] * ws[e]
+                good = (src[a:b] >= 0) & (src[a:b] < T)
+                want[a:b] = torch.where(good[:, None], y.to(dtype), want[a:b])
+        assert torch.equal(out, want), (lengths[:8], E, N, K)
+    for tile in ("256x256", "128x256", "128x128", "64x128"):
+        assert f"kernel=tile tile={tile}" in seen, seen
+
+
+@pytest.mark.parametrize("seed", range(6))
+def test_grouped_tiles_bad_offsets_stay_within_the_buffers(seed):
+    """Offsets in any order and far out of range, on the tile kernels: what is
+    around the output stays as it was."""
+    E, R, N, K = 40, 9000, 1100, 96
+    off = torch.randint(-2 ** 31, 2 ** 31 - 1, (E + 1,), generator=gen(seed)) if seed % 2 else torch.randint(-500, R + 500, (E + 1,), generator=gen(seed))
+    assert "kernel=tile" in kernel_of(R, N, K, E)
+    xq, xs, wq, ws = codes(R, K, 1), scales(R, 2), codes(E * N, K, 3).view(E, N, K), scales(E * N, 4).view(E, N)
+    store = torch.full((R + 600, N), 3.0, dtype=BF16, device=DEV)
+    mmq.grouped_gemm_i8(xq, xs, wq, ws, off.to(torch.int32).to(DEV), out=store[300:300 + R])
+    assert bool((store[:300] == 3.0).all()) and bool((store[300 + R:] == 3.0).all())
 
 
 @pytest.mark.parametrize("lengths", [[4, 9, 3], [40, 150, 30]], ids=["few", "many"])

@@ -95,6 +95,12 @@ def test_plan_refusals(M, N, K, E, why):
     assert not mmq.plan_i8(64, 64, 64, 0, 0)[0]
 
 
+@pytest.mark.parametrize("M,N,why", [((1 << 31) - 100, 8, "2^31 rows"), (16, (1 << 31) - 100, "2^32"), (16, 1 << 30, "2^32")])
+def test_plan_refuses_what_a_launch_cannot_hold(M, N, why):
+    ok, desc = mmq.plan_i8(M, N, 16, 0, 256)
+    assert not ok and why in desc, desc
+
+
 @pytest.mark.parametrize("E", [0, 1, 5, 128, 2048])
 @pytest.mark.parametrize("M,N", [(1, 1), (1, 3584), (8, 1536), (13, 18944), (64, 512), (65, 65), (509, 4608), (2048, 3584),
                                  (8192, 18944), (12008, 2048), (16384, 1536)])
