@@ -176,24 +176,33 @@ __global__ __launch_bounds__(THREADS < 256 ? 256 : THREADS) void k_quantize_i8(
 // GEMM
 // ---------------------------------------------------------------------------
 
-// Inclusive scans over the lanes of a wave.
+// Inclusive scans of numbers >= 0 over the lanes of a wave, by DPP: shifts
+// within the rows of 16 lanes, then each row's last lane to the rows behind.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ int dpp_or_0(int v) {
+    return __builtin_amdgcn_update_dpp(0, v, CTRL, ROWS, 0xf, false);
+}
 __device__ __forceinline__ int scan_sum(int v) {
-    const int lane = threadIdx.x & 63;
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-        const int u = __shfl_up(v, o);
-        if (lane >= o) v += u;
-    }
+    v += dpp_or_0<0x111, 0xf>(v);      // row_shr:1
+    v += dpp_or_0<0x112, 0xf>(v);
+    v += dpp_or_0<0x114, 0xf>(v);
+    v += dpp_or_0<0x118, 0xf>(v);
+    v += dpp_or_0<0x142, 0xa>(v);      // row_bcast:15 into rows 1 and 3
+    v += dpp_or_0<0x143, 0xc>(v);      // row_bcast:31 into rows 2 and 3
     return v;
 }
 __device__ __forceinline__ int scan_max(int v) {
-    const int lane = threadIdx.x & 63;
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-        const int u = __shfl_up(v, o);
-        if (lane >= o) v = max(v, u);
-    }
+    v = max(v, dpp_or_0<0x111, 0xf>(v));
+    v = max(v, dpp_or_0<0x112, 0xf>(v));
+    v = max(v, dpp_or_0<0x114, 0xf>(v));
+    v = max(v, dpp_or_0<0x118, 0xf>(v));
+    v = max(v, dpp_or_0<0x142, 0xa>(v));
+    v = max(v, dpp_or_0<0x143, 0xc>(v));
     return v;
+}
+// The lane before's v; `first` in lane 0.
+__device__ __forceinline__ int lane_before(int v, int first) {
+    return __builtin_amdgcn_update_dpp(first, v, 0x138, 0xf, 0xf, false);      // wave_shr:1
 }
 
 // The group that tile `tile` of a grouped launch belongs to: its expert and
@@ -210,8 +219,7 @@ __device__ __forceinline__ bool find_group(const int32_t *__restrict__ offsets, 
         int t = 0;
         if (e0 + lane < E) t = min(max(offsets[e0 + lane + 1], 0), M);
         t = max(scan_max(t), seen);
-        int b = __shfl_up(t, 1);
-        if (lane == 0) b = seen;
+        const int b = lane_before(t, seen);
         const int n = (t - b + TM - 1) / TM, upto = scan_sum(n);
         const unsigned long long hit = __ballot(before + upto > tile);
         if (hit) {
@@ -358,8 +366,7 @@ __device__ __forceinline__ int scan_groups(const I8Args &a, int *start, int *par
             most = max(most, part[w]);
         }
         t = max(t, last);
-        int b = __shfl_up(t, 1);
-        if (lane == 0) b = last;
+        const int b = lane_before(t, last);
         const int n = (t - b + TM - 1) / TM, upto = scan_sum(n);
         __syncthreads();
         if (lane == 63) part[wv] = upto;
