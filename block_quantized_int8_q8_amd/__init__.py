@@ -381,17 +381,20 @@ def _type_code(dtype) -> int:
     return code
 
 
-def _matrix(t, what, dtype=None, rows=None, cols=None, dev=None):
-    """Row pitch of the matrix ``t`` in elements; its columns must be adjacent."""
-    if t.dim() != 2:
-        raise ValueError(f"{what}: expected a matrix, got shape {tuple(t.shape)}")
+def _matrix(t, what, dtype, rows, cols, dev):
+    """Row pitch of the matrix ``t`` in elements; its columns must be adjacent.
+    ``dtype``, ``rows`` and ``cols`` are checked unless None."""
+    shape = t.shape
+    if len(shape) != 2:
+        raise ValueError(f"{what}: expected a matrix, got shape {tuple(shape)}")
     if dtype is not None and t.dtype is not dtype:
         raise ValueError(f"{what}: expected {dtype}, got {t.dtype}")
-    r, c = t.shape
+    r, c = shape
     if (rows is not None and r != rows) or (cols is not None and c != cols):
         raise ValueError(f"{what}: expected shape ({rows if rows is not None else r}, "
-                         f"{cols if cols is not None else c}), got {tuple(t.shape)}")
-    _on(t, what, dev)
+                         f"{cols if cols is not None else c}), got {tuple(shape)}")
+    if t.device != dev:
+        raise ValueError(f"{what} is on {t.device}, the other tensors on {dev}")
     if t.is_contiguous():
         return c
     sr, sc = t.stride()
@@ -403,21 +406,22 @@ def _matrix(t, what, dtype=None, rows=None, cols=None, dev=None):
 
 
 def _vector(t, what, dtype, n, dev):
+    """Address of the contiguous vector ``t`` of ``n`` elements."""
     if t.dtype is not dtype:
         raise ValueError(f"{what}: expected {dtype}, got {t.dtype}")
     if t.shape != (n,):
         raise ValueError(f"{what}: expected shape ({n},), got {tuple(t.shape)}")
-    _on(t, what, dev)
+    if t.device != dev:
+        raise ValueError(f"{what} is on {t.device}, the other tensors on {dev}")
     if not t.is_contiguous():
         raise ValueError(f"{what}: must be contiguous")
     return t.data_ptr()
 
 
-def _on(t, what, dev):
+def _gpu_of(t, what):
     if not t.is_cuda:
         raise ValueError(f"{what}: tensor must be on a GPU device")
-    if dev is not None and t.device != dev:
-        raise ValueError(f"{what} is on {t.device}, the other tensors on {dev}")
+    return t.device
 
 
 class _Calls:
@@ -492,9 +496,9 @@ def quantize_i8(x, q=None, scale=None, stream=None):
     """fp32/bf16/fp16 [M, K] -> (int8 codes [M, K rounded up to 16], fp32
     scales [M]): amax/127 per row (a token, or a weight's output channel).
     Padding codes are 0; a row with an infinity or NaN gets scale NaN."""
-    dev = x.device
+    dev = _gpu_of(x, "x")
     code = _type_code(x.dtype)
-    ldx = _matrix(x, "x")
+    ldx = _matrix(x, "x", None, None, None, dev)
     M, K = x.shape
     q, ldq, scale, sp = _codes_out(q, scale, M, K, dev, stream)
     _launch(_c().quantize, "mmq_quantize_i8", dev, stream, (x, q, scale), code, x.data_ptr(), ldx, q.data_ptr(), ldq,
@@ -505,9 +509,9 @@ def quantize_i8(x, q=None, scale=None, stream=None):
 def silu_mul_quantize_i8(gate, up, q=None, scale=None, stream=None):
     """silu(gate) * up ([M, K] each, e.g. the halves of one [M, 2K] matrix),
     quantized per row as by ``quantize_i8`` -> (codes, scales)."""
-    dev = gate.device
+    dev = _gpu_of(gate, "gate")
     code = _type_code(gate.dtype)
-    ld = _matrix(gate, "gate")
+    ld = _matrix(gate, "gate", None, None, None, dev)
     M, K = gate.shape
     if _matrix(up, "up", gate.dtype, M, K, dev) != ld:
         raise ValueError(f"gate and up must have the same row pitch, got strides {gate.stride()} and {up.stride()}")
@@ -533,8 +537,8 @@ def gemm_i8(xq, xs, wq, ws, bias=None, dtype=None, out=None, stream=None):
     channel (ws [N]), plus an optional fp32 bias [N] -> [M, N] of ``dtype``
     (float32 by default).  The integer sum is exact."""
     c = _c()
-    dev = xq.device
-    ldx = _matrix(xq, "xq", c.i8)
+    dev = _gpu_of(xq, "xq")
+    ldx = _matrix(xq, "xq", c.i8, None, None, dev)
     M, K = xq.shape
     ldw = _matrix(wq, "wq", c.i8, None, K, dev)
     N = wq.shape[0]
@@ -555,20 +559,20 @@ def grouped_gemm_i8(xq, xs, wq, ws, offsets, rows=None, dtype=None, out=None, st
     group, and rows whose index is out of range, are left as they were (in a
     fresh ``out``: undefined)."""
     c = _c()
-    dev = xq.device
-    ldx = _matrix(xq, "xq", c.i8)
+    dev = _gpu_of(xq, "xq")
+    ldx = _matrix(xq, "xq", c.i8, None, None, dev)
     T, K = xq.shape
     if wq.dim() != 3 or wq.dtype != c.i8:
         raise ValueError(f"wq: expected int8 [experts, N, K], got {wq.dtype} {tuple(wq.shape)}")
     E, N, Kw = wq.shape
     if Kw != K:
         raise ValueError(f"wq: expected rows of {K} codes, got {Kw}")
-    _on(wq, "wq", dev)
     if not wq.is_contiguous():
         raise ValueError("wq must be contiguous")
-    if tuple(ws.shape) != (E, N) or ws.dtype != c.f32 or not ws.is_contiguous():
+    if ws.shape != (E, N) or ws.dtype is not c.f32 or not ws.is_contiguous():
         raise ValueError(f"ws: expected contiguous float32 ({E}, {N}), got {ws.dtype} {tuple(ws.shape)}")
-    _on(ws, "ws", dev)
+    if wq.device != dev or ws.device != dev:
+        raise ValueError(f"wq is on {wq.device}, ws on {ws.device}, the other tensors on {dev}")
     xp = _vector(xs, "xs", c.f32, T, dev)
     op = _vector(offsets, "offsets", c.i32, E + 1, dev)
     R, rp = T, None
