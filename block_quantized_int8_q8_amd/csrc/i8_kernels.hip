@@ -431,12 +431,23 @@ __global__ __launch_bounds__(64 * WM * WN, OCC) void k_i8_tile(I8Args a, int til
     const int t_end = (xcd + 1) * (total / 8) + min(xcd + 1, total % 8);
     if (t >= t_end) return;
 
+    // What follows from the lane number outside the products is computed for
+    // every tile where the accumulators leave no room to keep it: kept, it
+    // spilled, and every reload waited for the DMA and the stores under way
+    // (8192 x 18944 x 3584 510 -> 495 us; smaller tiles are 1-2 % faster with it
+    // kept).
+    auto lane_anew = [&]() {
+        int l = lane;
+        if (AI * BJ >= 8) asm volatile("" : "+v"(l));
+        return l;
+    };
     // source chunk of this lane in DMA instruction u of an operand
-    auto chunk_of = [&](int u) { return 16 * ((lane & 7) ^ (((u * 8 + (lane >> 3)) >> 1) & 7)); };
+    auto chunk_of = [](int lane, int u) { return 16 * ((lane & 7) ^ (((u * 8 + (lane >> 3)) >> 1) & 7)); };
     int row0, end, e, n0, stored;          // stored: bit i, this lane's row of sub-tile i exists
     i32x4 rx, rw;
     uint32_t va[UA], vb[UB];
     auto setup = [&]() {                   // tile t
+        const int lane = lane_anew(), ml = lane & 31;
         const int size = kBand * tiles_n, b = t / size, r = t % size, hb = min(kBand, tiles_m - b * kBand);
         const int tm = b * kBand + r % hb;
         n0 = (r / hb) * BN;
@@ -457,11 +468,11 @@ __global__ __launch_bounds__(64 * WM * WN, OCC) void k_i8_tile(I8Args a, int til
             const int rh = (wv * UH + u % UH) * 8 + (lane >> 3);
             const int r = min((rh / HW) * 2 * HW + (u / UH) * HW + rh % HW, end - row0 - 1);
             const uint32_t src = gather ? uint32_t(max(source_row<GROUPED>(a, row0 + r), 0)) : uint32_t(r);
-            va[u] = src * uint32_t(a.ldx) + chunk_of(wv * UH + u % UH);
+            va[u] = src * uint32_t(a.ldx) + chunk_of(lane, wv * UH + u % UH);
         }
 #pragma unroll
         for (int u = 0; u < UB; u++)
-            vb[u] = uint32_t(min((wv * UB + u) * 8 + (lane >> 3), N - n0 - 1)) * uint32_t(a.ldw) + chunk_of(wv * UB + u);
+            vb[u] = uint32_t(min((wv * UB + u) * 8 + (lane >> 3), N - n0 - 1)) * uint32_t(a.ldw) + chunk_of(lane, wv * UB + u);
         stored = 0;
 #pragma unroll
         for (int i = 0; i < AI; i++) {
@@ -474,11 +485,11 @@ __global__ __launch_bounds__(64 * WM * WN, OCC) void k_i8_tile(I8Args a, int til
     // nothing.
     auto load1 = [&](int u, int k0, int stage) {
         if (u < UB) {
-            const bool in = k0 + chunk_of(wv * UB + u) < K;
+            const bool in = k0 + chunk_of(lane, wv * UB + u) < K;
             dma16(rw, lds0 + stage * STAGE + OFF_W + (wv * UB + u) * 1024, in ? vb[u < UB ? u : 0] : kNowhere, k0);
         } else {
             const int v = u - UB;
-            const bool in = k0 + chunk_of(wv * UH + v % UH) < K;
+            const bool in = k0 + chunk_of(lane, wv * UH + v % UH) < K;
             dma16(rx, lds0 + stage * STAGE + (v / UH) * (OFF_W / 2) + (wv * UH + v % UH) * 1024,
                   in ? va[v >= 0 && v < UA ? v : 0] : kNowhere, k0);
         }
@@ -492,6 +503,7 @@ __global__ __launch_bounds__(64 * WM * WN, OCC) void k_i8_tile(I8Args a, int til
         const i32x4 rs = wide_words(a.xs + (gather ? 0 : row0)), rv = wide_words(a.ws + int64_t(e) * N + n0);
         const i32x4 rb = wide_words(a.bias + n0);
         const uint32_t base = lds_scales + parity * SCALES * 4;
+        const int lane = lane_anew();
         for (int g = wv; g < BM / 64; g += W) {
             const int r = g * 64 + lane, src = row0 + r >= end ? -1 : gather ? source_row<GROUPED>(a, row0 + r) : r;
             dma4(rs, base + g * 256, src < 0 ? kNowhere : uint32_t(src) * 4);
@@ -607,6 +619,7 @@ __global__ __launch_bounds__(64 * WM * WN, OCC) void k_i8_tile(I8Args a, int til
         }
         full = false;
         if (active) {
+            const int ln = lane_anew(), ml = ln & 31, h = ln >> 5;
             const float *sxs = scales[parity], *sws = sxs + BM, *sbias = sws + BN;
             O *out = static_cast<O *>(a.out) + int64_t(o_row) * a.ldo + o_n;
             const int n_left = N - o_n;
@@ -630,7 +643,7 @@ __global__ __launch_bounds__(64 * WM * WN, OCC) void k_i8_tile(I8Args a, int til
                     }
 #pragma unroll
                     for (int it = 0; it < CH / 2; it++) {
-                        const int row = it * (64 / CH) + lane / CH, ck = lane % CH, n = cc * CW + ck * PER;
+                        const int row = it * (64 / CH) + ln / CH, ck = ln % CH, n = cc * CW + ck * PER;
                         const i32x4 v = *reinterpret_cast<const i32x4 *>(slab + row * RB + 16 * (ck ^ (row & (CH - 1))));
                         O *p = out + int64_t(32 * i + row) * a.ldo + n;
                         if (full)

@@ -64,7 +64,7 @@ struct I8KernelInfo {
     double step_us, fixed_us;
 };
 constexpr I8KernelInfo kI8Kernels[I8_KERNELS] = {
-    {"tile", 256, 256, 512, 1, 1.45, 9.5}, {"tile", 128, 256, 512, 1, 0.87, 5.5}, {"tile", 128, 128, 256, 2, 0.51, 3.0},
+    {"tile", 256, 256, 512, 1, 1.40, 9.0}, {"tile", 128, 256, 512, 1, 0.87, 5.5}, {"tile", 128, 128, 256, 2, 0.51, 3.0},
     {"tile", 64, 128, 256, 2, 0.30, 2.0},  {"rows", 16, 16, 256, 0, 0.0, 0.0},    {"rows", 16, 32, 256, 0, 0.0, 0.0},
     {"rows", 32, 32, 256, 0, 0.0, 0.0},    {"rows", 32, 64, 256, 0, 0.0, 0.0},    {"rows", 64, 64, 256, 0, 0.0, 0.0},
 };
