@@ -44,14 +44,14 @@ def _code_only(text: str) -> str:
 
 
 def source_hash() -> str:
-    """Hash of the kernel sources' code (comments and layout ignored): the
-    committed HBM-traffic counters are reported only while it matches."""
+    """Hash of the code (comments and layout ignored) of the kernels whose
+    HBM-traffic counters are committed, the block formats', and of their
+    launch plans: the counters are reported only while it matches."""
     h = hashlib.sha256()
     csrc = os.path.join(ROOT, "block_quantized_int8_q8_amd", "csrc")
-    for name in sorted(os.listdir(csrc)):
-        if name.endswith((".hip", ".hpp")):
-            h.update(name.encode())
-            h.update(_code_only(open(os.path.join(csrc, name)).read()).encode())
+    for name in ("mmq_kernels.hip", "mmq_plan.hpp"):
+        h.update(name.encode())
+        h.update(_code_only(open(os.path.join(csrc, name)).read()).encode())
     return h.hexdigest()[:16]
 
 

@@ -336,6 +336,9 @@ int mmq_moe_gemm_noalloc(int fmt, const void *x_q8_1, const void *w, int n_exper
  * rounded up to 16, for the quantizers' output) are neither read nor written.
  * K <= MMQ_I8_MAX_K keeps the int32 sum of a row exact for any codes, -128
  * included.  Sizes of zero rows (M = 0, R = 0) return 1 and launch nothing.
+ * These entry points keep no state and need no workspace: calls may overlap
+ * in time on any streams, and be captured into graphs and replayed (a
+ * grouping is read from the device at every replay).
  * The other conventions are those at the top of this file.
  * ------------------------------------------------------------------------- */
 #define MMQ_TYPE_F32 0
@@ -387,7 +390,7 @@ int mmq_gemm_i8(int type, const void *xq, int64_t ldx, const float *xs, const vo
  * they were, and so is a row whose rows[r] lies outside 0..T-1.  Offsets are
  * clamped to 0..R; with decreasing ones it is unspecified which rows of out
  * are written, but nothing outside the buffers is read or written.
- * 1 <= n_experts <= 2048. */
+ * 1 <= n_experts <= 2048; with rows, T * ldx is at most 4 GiB less 4 KiB. */
 int mmq_grouped_gemm_i8(int type, const void *xq, int64_t ldx, const float *xs, int64_t T, const int32_t *rows,
                         const int32_t *offsets, int n_experts, const void *wq, int64_t ldw, const float *ws, void *out,
                         int64_t ldo, int64_t R, int64_t N, int64_t K, void *stream);

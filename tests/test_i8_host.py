@@ -54,7 +54,7 @@ CALLS = {
         (dict(E=0), "n_experts"), (dict(E=2049), "n_experts"), (dict(T=-1), "T must"), (dict(T=3), "no row index"),
         (dict(T=0, rows=OK), "gather"), (dict(offsets=None), "null"), (dict(offsets=OK + 2), "4-byte"),
         (dict(rows=OK + 1), "4-byte"), (dict(K=40), "multiple of 16"), (dict(R=-1), "M must"), (dict(w=None), "null"),
-        (dict(type=3), "type"), (dict(ldo=8), "shorter")]),
+        (dict(type=3), "type"), (dict(ldo=8), "shorter"), (dict(T=1 << 20, ldx=1 << 16, rows=OK), "4 GiB")]),
 }
 REFUSALS = [(n, kw, why) for n, (_, cases) in CALLS.items() for kw, why in cases]
 
