@@ -370,10 +370,6 @@ def debug_block_dots(fmt, xq, w, M, N, K, dots=None, stream=None):
 I8_MAX_K = 131056
 
 
-def _pad16(K) -> int:
-    return (K + 15) // 16 * 16
-
-
 def _type_code(dtype) -> int:
     code = _c().codes.get(dtype)
     if code is None:
@@ -450,83 +446,84 @@ def _c() -> _Calls:
     return _calls
 
 
-def _empty(shape, dtype, dev, stream):
-    c = _c()
+def _empty(c, shape, dtype, dev, stream):
     if stream is None:
         return c.empty(shape, dtype=dtype, device=dev)
     with c.stream(stream):
         return c.empty(shape, dtype=dtype, device=dev)
 
 
-def _launch(fn, name, dev, stream, tensors, *args):
-    """Call ``fn`` on ``dev`` (made current for the call) and its stream;
-    ``tensors``: what it reads and writes."""
-    c = _c()
+def _stream_for(c, dev, stream, *tensors):
+    """Handle of the stream to launch on; ``tensors``: what the launch reads
+    and writes."""
     if stream is None:
-        s = c.raw_stream(dev.index)
-    elif stream.device == dev:
-        s = stream.cuda_stream
-        if s != c.raw_stream(dev.index):
-            for t in tensors:
-                if t is not None:
-                    t.record_stream(stream)
-    else:
+        return c.raw_stream(dev.index)
+    if stream.device != dev:
         raise ValueError(f"the stream is on {stream.device}, the tensors on {dev}")
-    if c.current_device() == dev.index:
-        rc = fn(*args, s)
-    else:
-        with c.device(dev):
-            rc = fn(*args, s)
-    if rc != 1:
-        raise MMQError(f"{name}: {last_error()}")
+    if stream.cuda_stream != c.raw_stream(dev.index):
+        for t in tensors:
+            if t is not None:
+                t.record_stream(stream)
+    return stream.cuda_stream
 
 
-def _codes_out(q, scale, M, K, dev, stream):
-    c = _c()
-    Kp = _pad16(K)
+def _codes_out(c, q, scale, M, K, dev, stream):
+    Kp = (K + 15) // 16 * 16
     if q is None:
-        q = _empty((M, Kp), c.i8, dev, stream)
-    ldq = _matrix(q, "q", c.i8, M, Kp, dev)
+        q, ldq = _empty(c, (M, Kp), c.i8, dev, stream), Kp
+    else:
+        ldq = _matrix(q, "q", c.i8, M, Kp, dev)
     if scale is None:
-        scale = _empty((M,), c.f32, dev, stream)
-    return q, ldq, scale, _vector(scale, "scale", c.f32, M, dev)
+        scale = _empty(c, (M,), c.f32, dev, stream)
+    else:
+        _vector(scale, "scale", c.f32, M, dev)
+    return q, ldq, scale
 
 
 def quantize_i8(x, q=None, scale=None, stream=None):
     """fp32/bf16/fp16 [M, K] -> (int8 codes [M, K rounded up to 16], fp32
     scales [M]): amax/127 per row (a token, or a weight's output channel).
     Padding codes are 0; a row with an infinity or NaN gets scale NaN."""
+    c = _calls or _c()
     dev = _gpu_of(x, "x")
+    if c.current_device() != dev.index:
+        with c.device(dev):
+            return quantize_i8(x, q, scale, stream)
     code = _type_code(x.dtype)
     ldx = _matrix(x, "x", None, None, None, dev)
     M, K = x.shape
-    q, ldq, scale, sp = _codes_out(q, scale, M, K, dev, stream)
-    _launch(_c().quantize, "mmq_quantize_i8", dev, stream, (x, q, scale), code, x.data_ptr(), ldx, q.data_ptr(), ldq,
-            sp, M, K)
+    q, ldq, scale = _codes_out(c, q, scale, M, K, dev, stream)
+    if c.quantize(code, x.data_ptr(), ldx, q.data_ptr(), ldq, scale.data_ptr(), M, K,
+                  _stream_for(c, dev, stream, x, q, scale)) != 1:
+        raise MMQError(f"mmq_quantize_i8: {last_error()}")
     return q, scale
 
 
 def silu_mul_quantize_i8(gate, up, q=None, scale=None, stream=None):
     """silu(gate) * up ([M, K] each, e.g. the halves of one [M, 2K] matrix),
     quantized per row as by ``quantize_i8`` -> (codes, scales)."""
+    c = _calls or _c()
     dev = _gpu_of(gate, "gate")
+    if c.current_device() != dev.index:
+        with c.device(dev):
+            return silu_mul_quantize_i8(gate, up, q, scale, stream)
     code = _type_code(gate.dtype)
     ld = _matrix(gate, "gate", None, None, None, dev)
     M, K = gate.shape
     if _matrix(up, "up", gate.dtype, M, K, dev) != ld:
         raise ValueError(f"gate and up must have the same row pitch, got strides {gate.stride()} and {up.stride()}")
-    q, ldq, scale, sp = _codes_out(q, scale, M, K, dev, stream)
-    _launch(_c().silu_mul, "mmq_silu_mul_quantize_i8", dev, stream, (gate, up, q, scale), code, gate.data_ptr(),
-            up.data_ptr(), ld, q.data_ptr(), ldq, sp, M, K)
+    q, ldq, scale = _codes_out(c, q, scale, M, K, dev, stream)
+    if c.silu_mul(code, gate.data_ptr(), up.data_ptr(), ld, q.data_ptr(), ldq, scale.data_ptr(), M, K,
+                  _stream_for(c, dev, stream, gate, up, q, scale)) != 1:
+        raise MMQError(f"mmq_silu_mul_quantize_i8: {last_error()}")
     return q, scale
 
 
-def _product_out(out, dtype, M, N, dev, stream):
-    c = _c()
+def _product_out(c, out, dtype, M, N, dev, stream):
     if out is None:
         dtype = c.f32 if dtype is None else dtype
         code = _type_code(dtype)
-        return _empty((M, N), dtype, dev, stream), code, N
+        return _empty(c, (M, N), dtype, dev, stream), code, N
     if dtype is not None and out.dtype != dtype:
         raise ValueError(f"out: expected {dtype}, got {out.dtype}")
     return out, _type_code(out.dtype), _matrix(out, "out", None, M, N, dev)
@@ -536,8 +533,11 @@ def gemm_i8(xq, xs, wq, ws, bias=None, dtype=None, out=None, stream=None):
     """Codes [M, K] x codes [N, K] with fp32 scales per token (xs [M]) and per
     channel (ws [N]), plus an optional fp32 bias [N] -> [M, N] of ``dtype``
     (float32 by default).  The integer sum is exact."""
-    c = _c()
+    c = _calls or _c()
     dev = _gpu_of(xq, "xq")
+    if c.current_device() != dev.index:
+        with c.device(dev):
+            return gemm_i8(xq, xs, wq, ws, bias, dtype, out, stream)
     ldx = _matrix(xq, "xq", c.i8, None, None, dev)
     M, K = xq.shape
     ldw = _matrix(wq, "wq", c.i8, None, K, dev)
@@ -545,9 +545,10 @@ def gemm_i8(xq, xs, wq, ws, bias=None, dtype=None, out=None, stream=None):
     xp = _vector(xs, "xs", c.f32, M, dev)
     wp = _vector(ws, "ws", c.f32, N, dev)
     bp = None if bias is None else _vector(bias, "bias", c.f32, N, dev)
-    out, code, ldo = _product_out(out, dtype, M, N, dev, stream)
-    _launch(c.gemm, "mmq_gemm_i8", dev, stream, (xq, xs, wq, ws, bias, out), code, xq.data_ptr(), ldx, xp, wq.data_ptr(),
-            ldw, wp, bp, out.data_ptr(), ldo, M, N, K)
+    out, code, ldo = _product_out(c, out, dtype, M, N, dev, stream)
+    if c.gemm(code, xq.data_ptr(), ldx, xp, wq.data_ptr(), ldw, wp, bp, out.data_ptr(), ldo, M, N, K,
+              _stream_for(c, dev, stream, xq, xs, wq, ws, bias, out)) != 1:
+        raise MMQError(f"mmq_gemm_i8: {last_error()}")
     return out
 
 
@@ -558,11 +559,14 @@ def grouped_gemm_i8(xq, xs, wq, ws, offsets, rows=None, dtype=None, out=None, st
     [E + 1] and ``rows`` int32 [R] stay on the device.  Rows outside every
     group, and rows whose index is out of range, are left as they were (in a
     fresh ``out``: undefined)."""
-    c = _c()
+    c = _calls or _c()
     dev = _gpu_of(xq, "xq")
+    if c.current_device() != dev.index:
+        with c.device(dev):
+            return grouped_gemm_i8(xq, xs, wq, ws, offsets, rows, dtype, out, stream)
     ldx = _matrix(xq, "xq", c.i8, None, None, dev)
     T, K = xq.shape
-    if wq.dim() != 3 or wq.dtype != c.i8:
+    if wq.dim() != 3 or wq.dtype is not c.i8:
         raise ValueError(f"wq: expected int8 [experts, N, K], got {wq.dtype} {tuple(wq.shape)}")
     E, N, Kw = wq.shape
     if Kw != K:
@@ -579,9 +583,10 @@ def grouped_gemm_i8(xq, xs, wq, ws, offsets, rows=None, dtype=None, out=None, st
     if rows is not None:
         R = rows.numel()
         rp = _vector(rows, "rows", c.i32, R, dev)
-    out, code, ldo = _product_out(out, dtype, R, N, dev, stream)
-    _launch(c.grouped, "mmq_grouped_gemm_i8", dev, stream, (xq, xs, wq, ws, offsets, rows, out), code, xq.data_ptr(), ldx,
-            xp, T, rp, op, E, wq.data_ptr(), K, ws.data_ptr(), out.data_ptr(), ldo, R, N, K)
+    out, code, ldo = _product_out(c, out, dtype, R, N, dev, stream)
+    if c.grouped(code, xq.data_ptr(), ldx, xp, T, rp, op, E, wq.data_ptr(), K, ws.data_ptr(), out.data_ptr(), ldo, R,
+                 N, K, _stream_for(c, dev, stream, xq, xs, wq, ws, offsets, rows, out)) != 1:
+        raise MMQError(f"mmq_grouped_gemm_i8: {last_error()}")
     return out
 
 

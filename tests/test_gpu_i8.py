@@ -518,6 +518,31 @@ def test_inputs_of_a_call_on_another_stream_are_kept_until_it_ran():
     assert torch.equal(out, want) and len(junk) == 8
 
 
+def test_tensors_of_a_gpu_that_is_not_current(monkeypatch):
+    """Each call makes the tensors' GPU current for itself (here the first
+    answer of the device query is another one)."""
+    c = mmq._c()
+    real, entered = c.current_device, []
+    device = c.device
+
+    def make_current(dev):
+        entered.append(dev)
+        return device(dev)
+
+    xq, xs, wq, ws = codes(5, 64, 1), scales(5, 2), codes(9, 64, 3), scales(9, 4)
+    x = torch.randn((5, 64), device=DEV)
+    off = torch.tensor([0, 5], dtype=torch.int32, device=DEV)
+    calls = [lambda: mmq.gemm_i8(xq, xs, wq, ws), lambda: mmq.quantize_i8(x)[0], lambda: mmq.silu_mul_quantize_i8(x, x)[0],
+             lambda: mmq.grouped_gemm_i8(xq, xs, wq[None], ws[None], off)]
+    for f in calls:
+        want = f()
+        answers = iter([real() + 1])
+        monkeypatch.setattr(c, "current_device", lambda: next(answers, real()))
+        monkeypatch.setattr(c, "device", make_current)
+        assert torch.equal(f(), want) and entered.pop() == xq.device
+        monkeypatch.undo()
+
+
 def test_no_rows():
     z = torch.empty((0, 64), dtype=BF16, device=DEV)
     q, s = mmq.quantize_i8(z)
