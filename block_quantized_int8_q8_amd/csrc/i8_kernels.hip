@@ -3,9 +3,10 @@
 //
 //   k_quantize_i8   rows of fp32 / bf16 / fp16 (or silu(gate) * up) -> int8
 //                   codes and one fp32 scale per row
-//   k_gemm_i8       int8 x int8 -> fp32 / bf16 / fp16 with a scale per row
+//   k_i8_tile       int8 x int8 -> fp32 / bf16 / fp16 with a scale per row
 //                   (token) and per column (channel), dense or grouped by
-//                   expert
+//                   expert, in tiles of 64 x 128 to 256 x 256 outputs
+//   k_i8_rows       the same for few rows or few tiles, down to one token
 //
 // With one scale per row of each operand the integer sum runs over all of K:
 //     out[m,n] = xs[m] * ws[n] * sum_k xq[m,k] * wq[n,k]
@@ -13,7 +14,6 @@
 // the scales are applied once per output element.  Integer sums are exact in
 // any order: how K is split never changes a result.
 #include <hip/hip_runtime.h>
-#include <hip/hip_fp16.h>
 #include <stdint.h>
 
 #include <type_traits>
@@ -270,8 +270,9 @@ __device__ __forceinline__ O scaled(int sum, float xs, float ws, float bias, boo
 // What bounds it.  Built without its products the kernel moves tiles at
 // 12-14 TB/s out of the L2s, of which a quarter misses them; without its DMA
 // it runs at 3.6 POP/s; both together, at the full chip's power-limited clock
-// (1.7-2.0 GHz under this load), it reaches 2.1.  So the schedule has to keep
-// loads in flight all the time and let no wave wait for LDS:
+// (1.7-2.0 GHz under this load), it reaches 2.2-2.3 (8192 x 18944 x 3584) to
+// 2.6 (8192 x 8192 x 8192).  So the schedule has to keep loads in flight all
+// the time and let no wave wait for LDS:
 //
 //  - A step's products run in two phases, first half of the tile's rows, then
 //    the second, and the weights' fragments of the whole step stay in
