@@ -319,6 +319,24 @@ def test_grouped_equals_dense_bit_for_bit():
             assert torch.equal(out[a:b], mmq.gemm_i8(xq[a:b], xs[a:b], wq[e], ws[e], dtype=BF16))
 
 
+@pytest.mark.parametrize("R", [40, 5000])
+def test_grouped_weights_beyond_4_gib(R):
+    """Experts whose matrices lie past 2^32 bytes, on the rows and the tile kernel."""
+    E, N, K = 300, 4096, 4096
+    wq = torch.zeros((E, N, K), dtype=torch.int8, device=DEV)
+    ws = torch.ones((E, N), device=DEV)
+    for e in (0, E - 1):
+        wq[e], ws[e] = codes(N, K, e), scales(N, e + 1)
+    off = torch.full((E + 1,), R // 2, dtype=torch.int32, device=DEV)
+    off[0], off[E] = 0, R
+    assert ("rows" if R == 40 else "tile") in kernel_of(R, N, K, E)
+    xq, xs = codes(R, K, 1), scales(R, 2)
+    out = mmq.grouped_gemm_i8(xq, xs, wq, ws, off)
+    for e, a, b in ((0, 0, R // 2), (E - 1, R // 2, R)):
+        acc = torch.matmul(xq[a:b].double(), wq[e].double().t())
+        assert torch.equal(out[a:b], acc.float() * xs[a:b, None] * ws[e])
+
+
 # ---------------------------------------------------------------------------
 # row quantizers
 # ---------------------------------------------------------------------------
@@ -405,6 +423,17 @@ def test_silu_mul_quantize(M, K, dtype):
     err = (q.cpu()[:, :K].double() * step - h).abs()
     assert bool((err <= step * (0.5 + 127 * 16 * U)).all())
     assert bool((q[:, K:] == 0).all())
+
+
+def test_quantize_beyond_32_bit_offsets():
+    """2.3 * 10^9 values: the last rows like the same rows alone."""
+    M, K = 70_001, 32_768
+    x = torch.zeros((M, K), dtype=BF16, device=DEV)
+    x[-3:] = torch.randn((3, K), generator=gen(1)).to(BF16).to(DEV)
+    q, s = mmq.quantize_i8(x)
+    wq, ws = mmq.quantize_i8(x[-3:].clone())
+    assert torch.equal(q[-3:], wq) and torch.equal(s[-3:], ws) and bool(ws.gt(0).all())
+    assert bool((s[:-3] == 0).all()) and bool((q[:-3] == 0).all())
 
 
 def test_silu_mul_special_rows():
