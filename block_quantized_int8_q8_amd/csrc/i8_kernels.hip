@@ -68,7 +68,10 @@ __device__ __forceinline__ void load_chunk(const T *row, int c, int K, float (&v
 
 // v = silu(v) * u = v / (1 + exp(-v)) * u.  exp(-v) = 2^t * 2^lo with t =
 // -v * log2(e) rounded to fp32 and lo what the rounding and the constant left
-// out (2^lo = 1 + lo * ln 2 to fp32: |lo| < 2^-16): an ulp or two of error.
+// out (2^lo = 1 + lo * ln 2 to fp32: |lo| < 2^-15): an ulp or two of error.
+// The exponential takes v limited to 200 in magnitude, past which it is 0
+// beside the 1, or the result is: the largest v would make t infinite and lo
+// NaN.
 // The quotient is the hardware's reciprocal with a residual correction: half
 // an ulp.  Where exp(-v) nears the largest number the 1 is far below its last
 // bit: v * exp(v), the exponential scaled by 2^64 to stay a normal number.
@@ -82,15 +85,15 @@ __device__ __forceinline__ void silu_mul(float (&v)[kChunk], const float (&u)[kC
     if (least > -86.0f) {
 #pragma unroll
         for (int i = 0; i < kChunk; i++) {
-            const float g = v[i], t = -g * L, lo = fmaf(-g, L_LO, fmaf(-g, L, -t)), x = __builtin_amdgcn_exp2f(t);
-            const float s = 1.0f + fmaf(x, lo * LN2, x), r = __builtin_amdgcn_rcpf(s), y = g * r;
+            const float g = v[i], c = fminf(g, 200.0f), t = -c * L, lo = fmaf(-c, L_LO, fmaf(-c, L, -t));
+            const float x = __builtin_amdgcn_exp2f(t), s = 1.0f + fmaf(x, lo * LN2, x), r = __builtin_amdgcn_rcpf(s), y = g * r;
             v[i] = fmaf(fmaf(-s, y, g), r, y) * u[i];
         }
     } else {
 #pragma unroll
         for (int i = 0; i < kChunk; i++) {
-            const float g = v[i], t = g * L, lo = fmaf(g, L_LO, fmaf(g, L, -t)), x = __builtin_amdgcn_exp2f(t + 64.0f);
-            const float far = g * fmaf(x, lo * LN2, x) * 0x1p-64f, s = 1.0f + expf(-g);
+            const float g = v[i], c = fmaxf(g, -200.0f), t = c * L, lo = fmaf(c, L_LO, fmaf(c, L, -t));
+            const float x = __builtin_amdgcn_exp2f(t + 64.0f), far = g * fmaf(x, lo * LN2, x) * 0x1p-64f, s = 1.0f + expf(-g);
             v[i] = (g > -86.0f ? g / s : far) * u[i];
         }
     }

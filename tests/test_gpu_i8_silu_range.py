@@ -1,0 +1,53 @@
+"""silu(gate) * up of the per-token int8 form over the whole range of finite
+gates, against 64 bits.
+
+Bounds.  u = 2^-24.  A value h = silu(g) * up is within 10 u |h| of the exact
+one (the exponential within 2 u, the sum, the quotient and the product u each,
+doubled for the products of those); where silu(g) itself is subnormal its
+rounding, 2^-150, adds up to 2^-149 |up|, doubled likewise.  A row's scale
+takes u more for the division by 127.  A code is within half a step of h / d,
+plus 127 times the relative errors of h, d and 1 / d."""
+import pytest
+import torch
+
+import block_quantized_int8_q8_amd as mmq
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+F32, BF16, F16 = torch.float32, torch.bfloat16, torch.float16
+U = 2.0 ** -24
+
+
+def check(g, u):
+    """Quantize silu(g) * u of the CPU tensors on the GPU and compare."""
+    K = g.shape[1]
+    q, s = mmq.silu_mul_quantize_i8(g.to(DEV), u.to(DEV))
+    q, s = q.cpu(), s.cpu().double()
+    g, u = g.double(), u.double()
+    h = g * torch.sigmoid(g) * u
+    tiny = 2.0 ** -149 * u.abs()
+    d = h.abs().amax(1) / 127
+    assert bool(s.isfinite().all()), s
+    assert bool(((s - d).abs() <= 11 * U * d + tiny.amax(1) / 127).all()), (s, d)
+    err = (q[:, :K].double() * s[:, None] - h).abs()
+    assert bool((err <= s[:, None] * (0.5 + 127 * 16 * U) + tiny).all())
+    assert bool((q[:, K:] == 0).all())
+
+
+@pytest.mark.parametrize("K", [24, 2100, 9000])
+@pytest.mark.parametrize("dtype", [F32, BF16, F16])
+def test_largest_finite_gates(K, dtype):
+    """The largest and lowest finite gates beside ordinary ones: silu(g) is g,
+    or -0 (the lowest value is what masks are filled with)."""
+    big = torch.finfo(dtype).max
+    small = 2.0 ** (-14 if dtype == F16 else -126)
+    rows = [(s * f * big, up) for s in (1, -1) for f in (1.0, 0.875, 0.703125, 0.5) for up in (0.25, -0.5, small)]
+    gen = torch.Generator().manual_seed(K)
+    g, u = torch.randn((len(rows), K), generator=gen).to(dtype), torch.randn((len(rows), K), generator=gen).to(dtype)
+    for i, (gate, up) in enumerate(rows):
+        at = (5 * i) % K
+        g[i, at], u[i, at] = gate, up
+    g[-1], u[-1] = -big, 1.0
+    g[-1, K // 2] = 1.5
+    assert bool(g.isfinite().all()) and bool(u.isfinite().all())
+    check(g, u)
