@@ -51,3 +51,20 @@ def test_largest_finite_gates(K, dtype):
     g[-1, K // 2] = 1.5
     assert bool(g.isfinite().all()) and bool(u.isfinite().all())
     check(g, u)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16, F16])
+def test_a_value_does_not_depend_on_its_neighbours(dtype):
+    """The same gate and up beside zeros, and beside gates of every size: the
+    value that sets the scale has the same bits."""
+    M, K = 4096, 16
+    gen = torch.Generator().manual_seed(3)
+    g, u = torch.zeros((M, K)), torch.full((M, K), 2.0 ** -20)
+    g[:, 3] = torch.rand(M, generator=gen) * 140 - (70 if dtype != F16 else 10)
+    u[:, 3] = 1 + torch.rand(M, generator=gen)
+    g, u = g.to(dtype), u.to(dtype)
+    want = mmq.silu_mul_quantize_i8(g.to(DEV), u.to(DEV))[1]
+    assert bool(want.gt(0).all())
+    for gate in (-90.0, -1000.0, float(torch.finfo(dtype).min)):
+        g[:, 6] = gate
+        assert torch.equal(mmq.silu_mul_quantize_i8(g.to(DEV), u.to(DEV))[1], want), gate
