@@ -362,7 +362,12 @@ int mmq_quantize_i8(int type, const void *x, int64_t ldx, void *q, int64_t ldq, 
  * an FFN's (or expert's) gate/up product and its down product, in one
  * reading of them.  gate, up: M x K of `type`, both with row pitch ld in
  * elements (gate and up may be the two halves of one M x 2K matrix).  The
- * value is gate / (1 + exp(-gate)) * up in fp32, not rounded to `type`. */
+ * value is gate / (1 + exp(-gate)) * up in fp32, not rounded to `type`: the
+ * quotient to a few units in its last place for every finite gate (below
+ * -88.7, where exp(-gate) alone would overflow, it is the small and in the end
+ * subnormal number that the exact quotient is, not -0), then one product.
+ * Its bits depend on its own gate and up only.  A value that is infinite or
+ * NaN (an infinite gate or up among the reasons) marks its row as there. */
 int mmq_silu_mul_quantize_i8(int type, const void *gate, const void *up, int64_t ld, void *q, int64_t ldq,
                              float *scale, int64_t M, int64_t K, void *stream);
 

@@ -68,3 +68,45 @@ def test_a_value_does_not_depend_on_its_neighbours(dtype):
     for gate in (-90.0, -1000.0, float(torch.finfo(dtype).min)):
         g[:, 6] = gate
         assert torch.equal(mmq.silu_mul_quantize_i8(g.to(DEV), u.to(DEV))[1], want), gate
+
+
+# (gates lo..hi, |up| to): exp(-gate) nears the largest number, and the result is what is small
+FAR = [(-80.0, -86.5, 2.0 ** 40), (-85.5, -89.0, 2.0 ** 60), (-87.0, -97.0, 2.0 ** 100), (-95.0, -104.0, 2.0 ** 120),
+       (-86.0, -103.0, 2.0 ** 127)]
+
+
+@pytest.mark.parametrize("among", ["alone", "ordinary", "large"])
+@pytest.mark.parametrize("dtype", [F32, BF16, F16])
+@pytest.mark.parametrize("lo,hi,top", FAR)
+def test_far_negative_gates_with_large_ups(lo, hi, top, dtype, among):
+    """Gates whose silu is tiny or subnormal with an up so large that they set
+    the scale: every value of the row, or one to three of each eight beside
+    ordinary or large positive gates."""
+    M, K = 64, 72
+    if dtype == F16:
+        top = 2.0 ** 15
+        hi = max(hi, -96.0)
+    gen = torch.Generator().manual_seed(int(-10 * hi))
+    far = lo + (hi - lo) * torch.rand((M, K), generator=gen)
+    big = top * (1 + torch.rand((M, K), generator=gen)) / 2 * torch.where(torch.rand((M, K), generator=gen) < 0.5, -1.0, 1.0)
+    if among == "alone":
+        g, u = far, big
+    else:
+        here = (torch.arange(K) % 8)[None, :] < torch.randint(1, 4, (M, 1), generator=gen)
+        near = torch.randn((M, K), generator=gen) * 2 if among == "ordinary" else 50 + 50 * torch.rand((M, K), generator=gen)
+        # so small that the far gates' values set the scale, about half of the time
+        least = 100 * float(torch.exp(torch.tensor(hi, dtype=torch.float64))) * top / 100
+        small = least * torch.exp(4 * torch.randn((M, K), generator=gen))
+        g, u = torch.where(here, far, near), torch.where(here, big, small)
+    check(g.to(dtype), u.to(dtype))
+
+
+def test_a_large_gate_sets_the_scale():
+    """silu(1000) = 1000 beside ordinary gates: scale and codes of the row."""
+    gen = torch.Generator().manual_seed(1)
+    g, u = torch.randn((3, 40), generator=gen), torch.randn((3, 40), generator=gen)
+    g[0, 3], g[1, 0], g[2, 39] = 1000.0, 87.0, -87.0
+    check(g, u)
+    s = mmq.silu_mul_quantize_i8(g.to(DEV), u.to(DEV))[1]
+    want = 1000.0 * float(u[0, 3].abs()) / 127
+    assert abs(float(s[0]) - want) <= 4 * U * want
