@@ -359,14 +359,22 @@ __device__ __forceinline__ void unrolled(F f) {
 template <int V> using constant = std::integral_constant<int, V>;
 
 // Row tiles of every expert, by the rule of find_group: start[e] becomes the
-// first tile of expert e, the sum is returned.
+// first tile of expert e, the sum is returned.  kLate marks an expert whose
+// rows start behind its own offset, at the end of a group before it: there
+// the offsets decrease.
+constexpr int kLate = INT32_MIN, kTile = INT32_MAX;
 template <int TM, int THREADS>
 __device__ __forceinline__ int scan_groups(const I8Args &a, int *start, int *part) {
     const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6, M = int(a.M);
     int tiles = 0, seen = min(max(a.offsets[0], 0), M);
     for (int e0 = 0; e0 < a.E; e0 += THREADS) {
         const int e = e0 + tid;
-        int t = scan_max(e < a.E ? min(max(a.offsets[e + 1], 0), M) : 0);
+        int own = 0, t = 0;                                        // the group's offset and the one behind it
+        if (e < a.E) {
+            own = min(max(a.offsets[e], 0), M);
+            t = min(max(a.offsets[e + 1], 0), M);
+        }
+        t = scan_max(t);
         if (lane == 63) part[wv] = t;
         __syncthreads();
         int last = seen, most = seen;                              // of the waves before this one, and of all
@@ -387,12 +395,18 @@ __device__ __forceinline__ int scan_groups(const I8Args &a, int *start, int *par
             if (w < wv) before += part[w];
             sum += part[w];
         }
-        if (e < a.E) start[e] = before + upto - n;
+        if (e < a.E) start[e] = (before + upto - n) | (b != own ? kLate : 0);
         tiles += sum;
         seen = most;
         __syncthreads();
     }
     return __builtin_amdgcn_readfirstlane(tiles);
+}
+// Where the rows of a late expert start: at the largest offset up to its own.
+__device__ __forceinline__ int late_row(const I8Args &a, int e) {
+    int t = 0;
+    for (int i = threadIdx.x & 63; i <= e; i += 64) t = max(t, min(max(a.offsets[i], 0), int(a.M)));
+    return __builtin_amdgcn_readlane(scan_max(t), 63);
 }
 // The expert of row tile `tile`: the last e with start[e] <= tile (of equal
 // starts only the last has tiles).  64-way search by one wave.
@@ -401,7 +415,7 @@ __device__ __forceinline__ int group_of(const int *start, int E, int tile) {
     int lo = 0, n = E;
     while (n > 1) {
         const int stride = (n + 63) / 64;
-        const bool ok = lane * stride < n && start[lo + lane * stride] <= tile;
+        const bool ok = lane * stride < n && (start[lo + lane * stride] & kTile) <= tile;
         const int c = __popcll(__ballot(ok)) - 1;
         lo += c * stride;
         n = min(stride, n - c * stride);
@@ -467,8 +481,9 @@ __global__ __launch_bounds__(64 * WM * WN, OCC) void k_i8_tile(I8Args a, int til
         if (GROUPED) {
             typedef const __attribute__((address_space(4))) int *scalar_ints;
             const scalar_ints off = (scalar_ints)a.offsets;
-            e = group_of(start, a.E, tm);          // (where offsets decrease, off[e] may lie before the group: still a row)
-            row0 = min(max(off[e], 0), end) + (tm - __builtin_amdgcn_readfirstlane(start[e])) * BM;
+            e = group_of(start, a.E, tm);
+            const int first = __builtin_amdgcn_readfirstlane(start[e]);
+            row0 = (first & kLate ? late_row(a, e) : min(max(off[e], 0), end)) + (tm - (first & kTile)) * BM;
             end = min(max(off[e + 1], 0), end);
         }
         rx = wide_words(a.x + (gather ? 0 : int64_t(row0) * a.ldx));

@@ -393,8 +393,9 @@ int mmq_gemm_i8(int type, const void *xq, int64_t ldx, const float *xs, const vo
  *   apart); ws: fp32 [n_experts][N]; out: R x N of `type`, pitch ldo.
  * Rows of out before offsets[0] or from offsets[n_experts] on are left as
  * they were, and so is a row whose rows[r] lies outside 0..T-1.  Offsets are
- * clamped to 0..R; with decreasing ones it is unspecified which rows of out
- * are written, but nothing outside the buffers is read or written.
+ * clamped to 0..R, and where they decrease a group starts where the furthest
+ * group before it ended: a row belongs to one group at most, and nothing
+ * outside the buffers is read or written.
  * 1 <= n_experts <= 2048; with rows, T * ldx is at most 4 GiB less 4 KiB. */
 int mmq_grouped_gemm_i8(int type, const void *xq, int64_t ldx, const float *xs, int64_t T, const int32_t *rows,
                         const int32_t *offsets, int n_experts, const void *wq, int64_t ldw, const float *ws, void *out,
