@@ -430,7 +430,10 @@ class _Calls:
         self.empty, self.device, self.stream = torch.empty, torch.cuda.device, torch.cuda.stream
         self.i8, self.f32, self.i32 = torch.int8, torch.float32, torch.int32
         self.codes = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
-        self.current_device, self.raw_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
+        # what the public calls read, without their own checks; a torch that has
+        # not these names has the public ones
+        self.current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+        self.raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", lambda i: torch.cuda.current_stream(i).cuda_stream)
         L = lib()
         self.quantize, self.silu_mul = L.mmq_quantize_i8, L.mmq_silu_mul_quantize_i8
         self.gemm, self.grouped = L.mmq_gemm_i8, L.mmq_grouped_gemm_i8
