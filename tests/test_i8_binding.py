@@ -6,22 +6,25 @@ import block_quantized_int8_q8_amd as mmq
 
 
 @pytest.fixture
-def public_names_only(monkeypatch):
-    for name in ("_cuda_getDevice", "_cuda_getCurrentRawStream"):
-        monkeypatch.delattr(torch._C, name, raising=False)
-    monkeypatch.setattr(mmq, "_calls", None)
+def calls(monkeypatch):
+    """What the binding looks up in a torch without two private names."""
+    with monkeypatch.context() as m:
+        for name in ("_cuda_getDevice", "_cuda_getCurrentRawStream"):
+            m.delattr(torch._C, name, raising=False)
+        c = mmq._Calls()
+    monkeypatch.setattr(mmq, "_calls", c)
+    return c
 
 
-def test_binding_without_torchs_private_names(public_names_only, monkeypatch):
+def test_binding_without_torchs_private_names(calls, monkeypatch):
     class Stream:
         cuda_stream = 77
     monkeypatch.setattr(torch.cuda, "current_stream", lambda i: Stream)
-    c = mmq._c()
-    assert c.current_device is torch.cuda.current_device and c.raw_stream(0) == 77
+    assert calls.current_device is torch.cuda.current_device and calls.raw_stream(0) == 77
 
 
 @pytest.mark.gpu
-def test_calls_without_torchs_private_names(public_names_only):
+def test_calls_without_torchs_private_names(calls):
     x = torch.randn((5, 64), generator=torch.Generator().manual_seed(1)).to("cuda:0")
     q, s = mmq.quantize_i8(x)
     side = torch.cuda.Stream()
