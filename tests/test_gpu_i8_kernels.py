@@ -118,3 +118,23 @@ def test_grouped(kernel, R, N, E, dtype, gather):
         r = r[(src[r] >= 0) & (src[r] < T)]
         want[r] = defined(xq[src[r]], xs[src[r]], wq[e], ws[e], None, dtype)
     assert torch.equal(out, want)
+
+
+@pytest.mark.parametrize("K", [3, 2049])
+def test_quantizers_of_more_rows_than_one_launch_holds(K):
+    """Rows 2^21 and on are another launch's: the last rows, and those around
+    the border, like the same rows alone; no row is left out."""
+    M = (1 << 21) + 5
+    x = torch.full((M, K), 0.5, dtype=torch.bfloat16, device=DEV)
+    picks = torch.tensor([0, (1 << 21) - 1, 1 << 21, M - 1], device=DEV)
+    x[picks] = torch.randn((4, K), generator=torch.Generator(device=DEV).manual_seed(K), device=DEV).to(torch.bfloat16)
+    rest = torch.ones(M, dtype=torch.bool, device=DEV)
+    rest[picks] = False
+    for call in (mmq.quantize_i8, lambda t: mmq.silu_mul_quantize_i8(t, t)):
+        q, s = call(x)
+        want, scale = call(x[picks])
+        assert torch.equal(q[picks], want) and torch.equal(s[picks], scale)
+        want, scale = call(x[1:2])
+        assert bool((s[rest] == scale).all()) and bool((q[:, :K].amin(1)[rest] == 127).all())
+        assert bool((q[:, K:] == 0).all())
+        del q, s, want
