@@ -77,8 +77,8 @@ __device__ __forceinline__ void load_chunk(const T *row, int c, int K, float (&v
 // A chunk of gates below 86 in magnitude needs neither that nor the limit
 // (which would change none of its values), and skips both: 2048 x 18944 bf16
 // over eight inputs in turn 45.3 us against 46.4.  Which form a value takes
-// depends on its own gate only.  With expf and a full divide everywhere: 8192 x 2047 bf16 19.4 us
-// against 17.7.
+// depends on its own gate only.  With expf and a full divide everywhere:
+// 8192 x 2047 bf16 19.4 us against 17.7.
 __device__ __forceinline__ void silu_mul(float (&v)[kChunk], const float (&u)[kChunk]) {
     constexpr float L = 1.44269502162933349609375f, L_LO = 1.92596299112661746887e-8f, LN2 = 0.693147182464599609375f;
     constexpr float FAR = 86.0f, LIMIT = 200.0f;
