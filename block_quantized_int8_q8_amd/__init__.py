@@ -25,6 +25,8 @@ EXPORTS = (
     "mmq_gemm_multi_ws", "mmq_moe_workspace_bytes",
     "mmq_moe_gemm", "mmq_moe_gemm_routed", "mmq_moe_gemm_noalloc", "mmq_debug_block_dots",
     "mmq_quantize_i8", "mmq_silu_mul_quantize_i8", "mmq_gemm_i8", "mmq_grouped_gemm_i8", "mmq_plan_i8",
+    "mmq_rope_frequencies", "mmq_rope", "mmq_kv_cache_bytes", "mmq_kv_write", "mmq_kv_read",
+    "mmq_attention_workspace_bytes", "mmq_attention_i8",
     "mmq_last_error", "mmq_plan_describe", "mmq_plan_for_limits",
     "mmq_debug_set_extra_lds", "mmq_version",
 )
@@ -80,6 +82,22 @@ def lib() -> ctypes.CDLL:
         L.mmq_grouped_gemm_i8.restype = i32
         L.mmq_plan_i8.argtypes = [i64, i64, i64, i32, i32, ctypes.c_char_p, i64]
         L.mmq_plan_i8.restype = i32
+        f64 = ctypes.c_double
+        L.mmq_rope_frequencies.argtypes = [i32, i32, f64, f64, f64, f64, i64, p, p]
+        L.mmq_rope_frequencies.restype = i32
+        L.mmq_rope.argtypes = [i32, p, i64, i64, i32, p, i64, i64, p, p, i32, i32, f64, i32, i64, i32, i32, p]
+        L.mmq_rope.restype = i32
+        L.mmq_kv_cache_bytes.argtypes = [i64, i32, i32, i32]
+        L.mmq_kv_cache_bytes.restype = i64
+        L.mmq_kv_write.argtypes = [i32, p, i64, i64, p, i64, i64, p, p, i32, i32, f64, p, i64, p, i64, i32, i32, i32, p]
+        L.mmq_kv_write.restype = i32
+        L.mmq_kv_read.argtypes = [i32, p, i64, i32, i32, i32, p, i64, p, i64, i64, p, i64, i64, p]
+        L.mmq_kv_read.restype = i32
+        L.mmq_attention_workspace_bytes.argtypes = [i64, i64, i64, i32, i32, i32, i64, i32]
+        L.mmq_attention_workspace_bytes.restype = i64
+        L.mmq_attention_i8.argtypes = [i32, p, i64, i64, p, i64, i32, p, i64, p, p, i64, i64, i64, i32, i32, i32,
+                                       ctypes.c_float, i64, i32, p, i64, i64, p, i64, p]
+        L.mmq_attention_i8.restype = i32
         L.mmq_debug_block_dots.argtypes = [i32, p, p, p, i64, i64, i64, p]
         L.mmq_debug_block_dots.restype = i32
         L.mmq_last_error.argtypes = []
@@ -428,7 +446,7 @@ class _Calls:
     def __init__(self):
         import torch
         self.empty, self.device, self.stream = torch.empty, torch.cuda.device, torch.cuda.stream
-        self.i8, self.f32, self.i32 = torch.int8, torch.float32, torch.int32
+        self.i8, self.f32, self.i32, self.bf16 = torch.int8, torch.float32, torch.int32, torch.bfloat16
         self.codes = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
         # what the public calls read, without their own checks; a torch that has
         # not these names has the public ones
@@ -437,6 +455,9 @@ class _Calls:
         L = lib()
         self.quantize, self.silu_mul = L.mmq_quantize_i8, L.mmq_silu_mul_quantize_i8
         self.gemm, self.grouped = L.mmq_gemm_i8, L.mmq_grouped_gemm_i8
+        self.f64, self.u8 = torch.float64, torch.uint8
+        self.rope, self.kv_write, self.kv_read = L.mmq_rope, L.mmq_kv_write, L.mmq_kv_read
+        self.attention, self.attention_bytes = L.mmq_attention_i8, L.mmq_attention_workspace_bytes
 
 
 _calls = None
@@ -598,6 +619,235 @@ def plan_i8(M, N, K, n_experts=0, cu_count=256) -> tuple[bool, str]:
     buf = ctypes.create_string_buffer(512)
     ok = lib().mmq_plan_i8(M, N, K, n_experts, cu_count, buf, 512)
     return bool(ok), buf.value.decode()
+
+
+# ---------------------------------------------------------------------------
+# Between a layer's q/k/v product and its output product: rotary positions, a
+# paged cache of keys and values in per-token int8, and attention of new
+# tokens over it.  Operands are [T, heads, D] with adjacent values and any
+# strides between tokens and heads (slices of a fused product's output, or
+# transposed views); devices and streams as for the calls above.
+# ---------------------------------------------------------------------------
+ROPE_HALF, ROPE_INTERLEAVED = 0, 1
+ROPE_SCALINGS = {None: 0, "linear": 1, "bands": 2, "yarn": 3}
+
+
+def _heads(t, what, dtype, shape, dev, written=False):
+    """Token and head strides of the [T, heads, D] operand ``t``; ``dtype`` and
+    the sizes in ``shape`` are checked unless None."""
+    if t.dim() != 3:
+        raise ValueError(f"{what}: expected [tokens, heads, values], got shape {tuple(t.shape)}")
+    if dtype is not None and t.dtype is not dtype:
+        raise ValueError(f"{what}: expected {dtype}, got {t.dtype}")
+    if shape is not None and any(n is not None and n != m for n, m in zip(shape, t.shape)):
+        raise ValueError(f"{what}: expected shape {tuple(m if n is None else n for n, m in zip(shape, t.shape))}, "
+                         f"got {tuple(t.shape)}")
+    if t.device != dev:
+        raise ValueError(f"{what} is on {t.device}, the other tensors on {dev}")
+    T, H, D = t.shape
+    if t.is_contiguous():
+        return H * D, D
+    st, sh, sd = t.stride()
+    if D > 1 and sd != 1:
+        raise ValueError(f"{what}: the values of a head must be adjacent (stride 1), got strides {t.stride()}")
+    # strides of a single token or head are never used, and torch leaves them as it likes
+    sh = sh if H > 1 else D
+    st = st if T > 1 else H * sh
+    if written and not (((H == 1 or sh >= D) and (T == 1 or st >= (H - 1) * sh + D))
+                        or ((T == 1 or st >= D) and (H == 1 or sh >= (T - 1) * st + D))):
+        raise ValueError(f"{what}: tokens or heads overlap (strides {t.stride()})")
+    return st, sh
+
+
+def rope_frequencies(rot, base=10000.0, scaling=None, factor=1.0, low=1.0, high=None, original=None):
+    """Rotary frequencies of ``rot`` values: (float64 [rot/2] on the host, the
+    factor mscale on rotated values).  ``scaling``: None, "linear", "bands" or
+    "yarn", for contexts ``factor`` times the ``original`` length; ``low`` and
+    ``high``: turns within it below which a frequency is scaled and above
+    which it is kept (default 1 and 4 for bands, 1 and 32 for yarn)."""
+    import torch
+    if scaling not in ROPE_SCALINGS:
+        raise ValueError(f"unknown scaling {scaling!r}: expected one of {list(ROPE_SCALINGS)}")
+    if high is None:
+        high = 32.0 if scaling == "yarn" else 4.0
+    freqs, mscale = torch.empty(max(int(rot) // 2, 1), dtype=torch.float64), ctypes.c_double()
+    _check(lib().mmq_rope_frequencies(ROPE_SCALINGS[scaling], rot, base, factor, low, high,
+                                      0 if original is None else original, ctypes.c_void_p(freqs.data_ptr()),
+                                      ctypes.byref(mscale)), "mmq_rope_frequencies")
+    return freqs, mscale.value
+
+
+def rope(x, positions, freqs, layout=ROPE_HALF, mscale=1.0, inverse=False, dtype=None, out=None, stream=None):
+    """[T, heads, D] with the first 2 len(freqs) values of every head turned by
+    its token's position (int32 [T]) times ``freqs`` (float64, on the GPU), of
+    ``dtype`` (x's by default).  ``out`` may be ``x``.  ``inverse`` turns back:
+    the rotation's gradient."""
+    c = _calls or _c()
+    dev = _gpu_of(x, "x")
+    if c.current_device() != dev.index:
+        with c.device(dev):
+            return rope(x, positions, freqs, layout, mscale, inverse, dtype, out, stream)
+    code = _type_code(x.dtype)
+    st, sh = _heads(x, "x", None, None, dev)
+    T, H, D = x.shape
+    pp = _vector(positions, "positions", c.i32, T, dev)
+    fp = _vector(freqs, "freqs", c.f64, freqs.numel(), dev)
+    if out is None:
+        out = _empty(c, (T, H, D), x.dtype if dtype is None else dtype, dev, stream)
+        ot, oh = H * D, D
+    else:
+        ot, oh = _heads(out, "out", dtype, (T, H, D), dev, written=True)
+    if c.rope(code, x.data_ptr(), st, sh, _type_code(out.dtype), out.data_ptr(), ot, oh, pp, fp, 2 * freqs.numel(), layout,
+              mscale, inverse, T, H, D, _stream_for(c, dev, stream, x, positions, freqs, out)) != 1:
+        raise MMQError(f"mmq_rope: {last_error()}")
+    return out
+
+
+def kv_cache_bytes(n_pages, page, heads, D) -> int:
+    """Bytes of an int8 cache of ``n_pages`` pages of ``page`` tokens."""
+    b = int(lib().mmq_kv_cache_bytes(n_pages, page, heads, D))
+    if b < 0:
+        raise MMQError(f"mmq_kv_cache_bytes: {last_error()}")
+    return b
+
+
+def kv_cache(n_pages, page, heads, D, device="cuda"):
+    """An int8 cache of ``n_pages`` pages of ``page`` tokens (16 .. 256) of
+    ``heads`` key/value heads of D values (64, 128 or 256): uint8 [n_pages,
+    heads, page * (2 D + 8)], its contents undefined until written."""
+    import torch
+    kv_cache_bytes(n_pages, page, heads, D)
+    return torch.empty((n_pages, heads, page * (2 * D + 8)), dtype=torch.uint8, device=device)
+
+
+def _cache(c, cache, D, dev):
+    """Pages, tokens of a page and heads of ``cache`` for heads of D values."""
+    if cache.dim() != 3 or cache.dtype is not c.u8 or not cache.is_contiguous():
+        raise ValueError(f"cache: expected contiguous uint8 [pages, heads, bytes], got {cache.dtype} {tuple(cache.shape)}")
+    if cache.device != dev:
+        raise ValueError(f"cache is on {cache.device}, the other tensors on {dev}")
+    n_pages, H, size = cache.shape
+    page, rest = divmod(size, 2 * D + 8)
+    if rest or page not in (16, 32, 64, 128, 256):
+        raise ValueError(f"cache: {size} bytes of a page and head are not those of 16..256 tokens of {D} values")
+    return n_pages, page, H
+
+
+def kv_write(k, v, cache, slots, positions=None, freqs=None, layout=ROPE_HALF, mscale=1.0, stream=None):
+    """Quantize keys and values ([T, heads, D] fp32/bf16/fp16) per token and
+    head and write them to their slots (int32 [T], all different; a token
+    whose slot is outside the cache, -1 say, is passed over).  With ``freqs``
+    and ``positions`` the keys are turned first, as by ``rope``."""
+    c = _calls or _c()
+    dev = _gpu_of(k, "k")
+    if c.current_device() != dev.index:
+        with c.device(dev):
+            return kv_write(k, v, cache, slots, positions, freqs, layout, mscale, stream)
+    code = _type_code(k.dtype)
+    kt, kh = _heads(k, "k", None, None, dev)
+    T, H, D = k.shape
+    vt, vh = _heads(v, "v", k.dtype, (T, H, D), dev)
+    n_pages, page, heads = _cache(c, cache, D, dev)
+    if heads != H:
+        raise ValueError(f"cache holds {heads} heads, k {H}")
+    sp = _vector(slots, "slots", c.i32, T, dev)
+    pp = fp = None
+    rot = 0
+    if freqs is not None:
+        if positions is None:
+            raise ValueError("freqs without positions")
+        rot = 2 * freqs.numel()
+        fp = _vector(freqs, "freqs", c.f64, freqs.numel(), dev)
+        pp = _vector(positions, "positions", c.i32, T, dev)
+    if c.kv_write(code, k.data_ptr(), kt, kh, v.data_ptr(), vt, vh, pp, fp, rot, layout, mscale, sp, T, cache.data_ptr(),
+                  n_pages, page, H, D, _stream_for(c, dev, stream, k, v, cache, slots, positions, freqs)) != 1:
+        raise MMQError(f"mmq_kv_write: {last_error()}")
+
+
+def kv_read(cache, slots, D, dtype=None, k=None, v=None, stream=None):
+    """The keys and values that slots (int32 [T], in any order) hold, as two
+    [T, heads, D] of ``dtype`` (bfloat16 by default).  Rows of a slot outside
+    the cache are left as they were (in fresh outputs: undefined)."""
+    c = _calls or _c()
+    dev = _gpu_of(cache, "cache")
+    if c.current_device() != dev.index:
+        with c.device(dev):
+            return kv_read(cache, slots, D, dtype, k, v, stream)
+    n_pages, page, H = _cache(c, cache, D, dev)
+    T = slots.numel()
+    sp = _vector(slots, "slots", c.i32, T, dev)
+    if dtype is None:
+        dtype = next((t.dtype for t in (k, v) if t is not None), c.bf16)
+    code = _type_code(dtype)
+    if k is None:
+        k, kt, kh = _empty(c, (T, H, D), dtype, dev, stream), H * D, D
+    else:
+        kt, kh = _heads(k, "k", dtype, (T, H, D), dev, written=True)
+    if v is None:
+        v, vt, vh = _empty(c, (T, H, D), dtype, dev, stream), H * D, D
+    else:
+        vt, vh = _heads(v, "v", dtype, (T, H, D), dev, written=True)
+    if c.kv_read(code, cache.data_ptr(), n_pages, page, H, D, sp, T, k.data_ptr(), kt, kh, v.data_ptr(), vt, vh,
+                 _stream_for(c, dev, stream, cache, slots, k, v)) != 1:
+        raise MMQError(f"mmq_kv_read: {last_error()}")
+    return k, v
+
+
+def attention_workspace_bytes(T, n_seqs, max_q, q_heads, kv_heads, D, max_pages, page) -> int:
+    """Device workspace bytes ``attention_i8`` needs on the current device."""
+    b = int(lib().mmq_attention_workspace_bytes(T, n_seqs, max_q, q_heads, kv_heads, D, max_pages, page))
+    if b < 0:
+        raise MMQError(f"mmq_attention_workspace_bytes: {last_error()}")
+    return b
+
+
+def attention_i8(q, cache, page_table, lens, q_offsets, max_q=None, scale=None, window=0, dtype=None, out=None,
+                 workspace=None, stream=None):
+    """Attention of new tokens ([T, query heads, D] bf16/fp16) over the cache
+    that already holds them -> [T, query heads, D] of ``dtype`` (q's, or
+    float32).  Sequence b: ``lens[b]`` tokens on the pages ``page_table[b]``,
+    the last ``q_offsets[b + 1] - q_offsets[b]`` of them new, rows q_offsets[b]..
+    of q; all int32, on the GPU.  ``max_q``: the most new tokens of a sequence
+    (T by default; 1 while decoding saves a launch); ``scale``: 1 / sqrt(D) by
+    default; ``window`` > 0: a token sees that many keys at most, itself among
+    them.  ``workspace``: uint8, attention_workspace_bytes long.  Rows outside
+    every sequence are left as they were (in a fresh ``out``: undefined)."""
+    c = _calls or _c()
+    dev = _gpu_of(q, "q")
+    if c.current_device() != dev.index:
+        with c.device(dev):
+            return attention_i8(q, cache, page_table, lens, q_offsets, max_q, scale, window, dtype, out, workspace, stream)
+    code = _type_code(q.dtype)
+    qt, qh = _heads(q, "q", None, None, dev)
+    T, Hq, D = q.shape
+    n_pages, page, Hkv = _cache(c, cache, D, dev)
+    B = lens.numel()
+    if (page_table.dim() != 2 or page_table.shape[0] != B or page_table.dtype is not c.i32 or page_table.device != dev
+            or not page_table.is_contiguous()):
+        raise ValueError(f"page_table: expected contiguous int32 [{B}, pages] on {dev}, got {page_table.dtype} "
+                         f"{tuple(page_table.shape)} on {page_table.device}")
+    max_pages = page_table.shape[1]
+    lp = _vector(lens, "lens", c.i32, B, dev)
+    op = _vector(q_offsets, "q_offsets", c.i32, B + 1, dev)
+    if out is None:
+        out = _empty(c, (T, Hq, D), q.dtype if dtype is None else dtype, dev, stream)
+        ot, oh = Hq * D, D
+    else:
+        ot, oh = _heads(out, "out", dtype, (T, Hq, D), dev, written=True)
+    if max_q is None:
+        max_q = max(T, 1)
+    if workspace is None:
+        need = c.attention_bytes(T, B, max_q, Hq, Hkv, D, max_pages, page)
+        if need > 0:
+            workspace = _empty(c, (need,), c.u8, dev, stream)
+    elif workspace.dtype is not c.u8 or workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError(f"workspace: expected contiguous uint8 on {dev}, got {workspace.dtype} on {workspace.device}")
+    wp, wn = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel())
+    if c.attention(code, q.data_ptr(), qt, qh, cache.data_ptr(), n_pages, page, page_table.data_ptr(), max_pages, lp, op, B, T,
+                   max_q, Hq, Hkv, D, D ** -0.5 if scale is None else scale, window, _type_code(out.dtype), out.data_ptr(), ot,
+                   oh, wp, wn, _stream_for(c, dev, stream, q, cache, page_table, lens, q_offsets, out, workspace)) != 1:
+        raise MMQError(f"mmq_attention_i8: {last_error()}")
+    return out
 
 
 def plan_describe(fmt, M, N, K) -> tuple[bool, str]:

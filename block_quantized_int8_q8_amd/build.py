@@ -9,7 +9,7 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libmmq.so")
-SOURCES = ["mmq_kernels.hip", "i8_kernels.hip", "mmq_api.hip"]
+SOURCES = ["mmq_kernels.hip", "i8_kernels.hip", "kv_kernels.hip", "attn_kernels.hip", "mmq_api.hip"]
 
 HIPCC_FLAGS = [
     "--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC", "-shared",

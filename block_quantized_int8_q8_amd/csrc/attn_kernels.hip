@@ -1,0 +1,738 @@
+// attn_kernels.hip -- gfx950 kernels of attention over the int8 paged cache.
+//
+//   k_attn_rows   sequences of few rows (decoding: one token, its group of
+//                 query heads): keys and values straight into registers
+//   k_attn_tile   sequences of many rows (a chunk of a prompt): keys and
+//                 values converted once per workgroup, through LDS
+//   k_attn_join   joins the shares of a sequence's keys that either split
+//
+// A row is one (new token, query head) pair; the rows of a sequence that read
+// the same key/value head are multiplied together.  With codes c and scales d
+// of the cache,
+//     s_t = scale * dk_t * (q . ck_t),   o = sum_t exp(s_t) dv_t cv_t / sum_t exp(s_t)
+// over the keys t that the row may see.  Codes are at most 127 in magnitude
+// and so exact in 16 bits: the two products run on the 16-bit matrix core
+// with q and the codes as they are, both scales are applied in fp32, and the
+// one rounding between q and the result is that of exp(s_t) dv_t to 16 bits
+// (the type of q), which the second product reads.  Sums, maxima and the
+// running output are fp32.
+//
+// Both products are formed transposed, keys (or value columns) by rows, so
+// that a lane holds scores of one row only: the maximum and the sum of a
+// softmax are per-lane numbers, and the scores' registers are, converted,
+// the second product's operand with no movement between lanes.
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include <type_traits>
+
+#include "attn_plan.hpp"
+#include "wave_scan.hpp"
+
+namespace mmq {
+
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+
+struct AttnArgs {
+    const void *q;            // [T, Hq, D]
+    int64_t qdt, qdh;
+    const uint8_t *cache;
+    const int32_t *table;     // [B, max_pages] pages
+    const int32_t *lens;      // [B] keys, the new tokens' own included
+    const int32_t *offsets;   // [B + 1] bounds of each sequence's new tokens
+    void *out;                // [T, Hq, D]
+    int64_t odt, odh;
+    int64_t n_pages, max_pages;
+    int page_shift, Hq, Hkv, G;
+    int T, B, max_q, window;
+    float scale;              // softmax scale times log2(e)
+    float *part;              // shares: outputs, then (reference, sum) pairs
+    int split, target;        // most shares; workgroups that fill the device
+    int units;                // rows kernel: B; tile kernel: row tiles there can be
+};
+
+// --- 16-bit types -----------------------------------------------------------
+template <typename T> struct Half;
+template <> struct Half<__bf16> {
+    typedef bf16x8 x8;
+    static constexpr bool NARROW = false;
+    static __device__ __forceinline__ f32x4 mfma16(x8 a, x8 b, f32x4 c) { return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0); }
+    static __device__ __forceinline__ f32x16 mfma32(x8 a, x8 b, f32x16 c) { return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0); }
+    // Four int8 codes as two dwords.  Integers below 256 have zeros in the low half of their fp32 form.
+    static __device__ __forceinline__ void codes(uint32_t c, uint32_t (&o)[2]) {
+        const uint32_t f0 = __float_as_uint(float(int8_t(c))), f1 = __float_as_uint(float(int8_t(c >> 8)));
+        const uint32_t f2 = __float_as_uint(float(int8_t(c >> 16))), f3 = __float_as_uint(float(int8_t(c >> 24)));
+        o[0] = __builtin_amdgcn_perm(f1, f0, 0x07060302u);
+        o[1] = __builtin_amdgcn_perm(f3, f2, 0x07060302u);
+    }
+};
+template <> struct Half<_Float16> {
+    typedef f16x8 x8;
+    static constexpr bool NARROW = true;         // exponents from -24 to 15 only
+    static __device__ __forceinline__ f32x4 mfma16(x8 a, x8 b, f32x4 c) { return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0); }
+    static __device__ __forceinline__ f32x16 mfma32(x8 a, x8 b, f32x16 c) { return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0); }
+    // code + 128 as the low bits of 1024 + code + 128, less 1152: exact.
+    static __device__ __forceinline__ void codes(uint32_t c, uint32_t (&o)[2]) {
+        const uint32_t u = c ^ 0x80808080u;
+        const f16x2 m = {_Float16(1152.0f), _Float16(1152.0f)};
+        o[0] = __builtin_bit_cast(uint32_t, __builtin_bit_cast(f16x2, __builtin_amdgcn_perm(0x64646464u, u, 0x04010400u)) - m);
+        o[1] = __builtin_bit_cast(uint32_t, __builtin_bit_cast(f16x2, __builtin_amdgcn_perm(0x64646464u, u, 0x04030402u)) - m);
+    }
+};
+
+template <typename T>
+__device__ __forceinline__ typename Half<T>::x8 codes8(uint32_t lo, uint32_t hi) {
+    uint32_t a[2], b[2];
+    Half<T>::codes(lo, a);
+    Half<T>::codes(hi, b);
+    const u32x4 v = {a[0], a[1], b[0], b[1]};
+    return __builtin_bit_cast(typename Half<T>::x8, v);
+}
+
+template <typename T>
+__device__ __forceinline__ typename Half<T>::x8 load_x8(const T *p) {
+    typename Half<T>::x8 v;
+    __builtin_memcpy(&v, p, 16);                 // rows may start at any multiple of the type's size
+    return v;
+}
+
+template <typename O>
+__device__ __forceinline__ void store4(O *p, f32x4 v) {
+    O t[4] = {O(v[0]), O(v[1]), O(v[2]), O(v[3])};
+    __builtin_memcpy(p, t, sizeof(t));
+}
+
+// --- sequences --------------------------------------------------------------
+struct Seq {
+    int start, n;             // rows of q: first new token, how many
+    int len, pos0;            // keys; position of the first new token (negative: it and those up to 0 see nothing)
+};
+
+__device__ __forceinline__ int clamp_row(const AttnArgs &a, int v) { return min(max(v, 0), a.T); }
+__device__ __forceinline__ int clamp_len(const AttnArgs &a, int v) {
+    return int(min(int64_t(max(v, 0)), a.max_pages << a.page_shift));
+}
+__device__ __forceinline__ Seq sequence(const AttnArgs &a, int b) {
+    const int s = clamp_row(a, a.offsets[b]), n = max(clamp_row(a, a.offsets[b + 1]) - s, 0);
+    const int len = clamp_len(a, a.lens[b]);
+    return Seq{s, min(n, a.max_q), len, len - n};
+}
+__device__ __forceinline__ bool has_few_rows(const AttnArgs &a, int n) { return int64_t(n) * a.G <= kAttnFewRows; }
+
+// The keys [begin, end) that tokens first .. last of a sequence see among
+// them; begin is rounded down to a tile of 16.
+struct Range {
+    int begin, end;
+    __device__ __forceinline__ Range(const AttnArgs &a, const Seq &s, int first, int last) {
+        end = max(s.pos0 + last + 1, 0);
+        begin = a.window ? max(s.pos0 + first - a.window + 1, 0) & ~15 : 0;
+        if (begin >= end) begin = end = 0;
+    }
+};
+
+// Tile number in the cache of 16-key tile k16 of sequence b, head h; -1 for a
+// page that the cache does not have.
+__device__ __forceinline__ int cache_tile(const AttnArgs &a, int b, int h, int k16) {
+    const int sh = a.page_shift - 4, page = a.table[int64_t(b) * a.max_pages + (k16 >> sh)];
+    if (uint32_t(page) >= uint32_t(a.n_pages)) return -1;
+    return ((page * a.Hkv + h) << sh) + (k16 & ((1 << sh) - 1));
+}
+
+__device__ __forceinline__ int wave_sum(int v) { return __builtin_amdgcn_readlane(scan_sum(v), 63); }
+__device__ __forceinline__ int wave_max(int v) { return __builtin_amdgcn_readlane(scan_max(v), 63); }
+
+// Keys of each share of the rows kernel: such that all few-row sequences'
+// shares together fill the device, at most `split` of them for the longest.
+__device__ __forceinline__ int few_chunk(const AttnArgs &a) {
+    const int lane = threadIdx.x & 63;
+    int most = 0;
+    float total = 0.0f;
+    for (int b0 = 0; b0 < a.B; b0 += 64) {
+        int k = 0;
+        if (b0 + lane < a.B) {
+            const Seq s = sequence(a, b0 + lane);
+            if (s.n > 0 && has_few_rows(a, s.n)) {
+                const Range r(a, s, 0, s.n - 1);
+                k = r.end - r.begin;
+            }
+        }
+        most = max(most, wave_max(k));
+        total += float(wave_sum(k >> 7)) + 1.0f;          // 128-key blocks
+    }
+    // a share of the keys of every head for each of the `target` workgroups
+    const float blocks = total * float(a.Hkv) / float(a.target);
+    const int by_device = int(fminf(blocks, 1e6f)) + 1, by_slots = ((most + a.split - 1) / a.split + 127) >> 7;
+    return max(max(by_device, by_slots), 1) << 7;
+}
+
+// ---------------------------------------------------------------------------
+// Softmax of the transposed scores in a lane's registers.
+//
+// Scores are in units of log2.  p = 2^(t - m) for a running reference m of
+// the row.  The second product's operand p * dv has the exponents of its type:
+// in bf16 any m near the maximum of t will do; in fp16 (NARROW) m is taken so
+// that the largest p * dv is between 2^6 and 2^14, whatever the size of dv:
+// m = max(t + log2 dv) - 6, but not so low that the sum of p leaves fp32
+// (m >= max(t) - 60: where that binds, the output is below 2^-47).  References
+// move up only, and only when a new maximum lies more than 2^8 above.
+// ---------------------------------------------------------------------------
+constexpr float kSlack = 8.0f;
+constexpr float kNarrowTop = 6.0f, kNarrowSum = 60.0f;
+
+// --- rows kernel ------------------------------------------------------------
+template <typename T, typename O, int D, int RT>
+__global__ __launch_bounds__(256) void k_attn_rows(AttnArgs a) {
+    typedef typename Half<T>::x8 x8;
+    constexpr int C = D / 64, TILE = int(kv_tile_bytes(D)), R = 16 * RT;
+    constexpr float NEG = -__builtin_inff();
+    __shared__ float S_o[4][R][68];
+    __shared__ float S_m[4][R], S_l[4][R];
+    const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), col = lane & 15, g = lane >> 4;
+    const int h = blockIdx.x % a.Hkv, rest = blockIdx.x / a.Hkv, b = rest % a.B, share = rest / a.B;
+    const Seq s = sequence(a, b);
+    const int rows = s.n * a.G;
+    if (s.n == 0 || !has_few_rows(a, s.n)) return;
+    const Range all(a, s, 0, s.n - 1);
+    int chunk = 0x7fffff80;
+    if (a.split > 1) chunk = few_chunk(a);
+    const int begin = all.begin + min(int64_t(share) * chunk, int64_t(all.end - all.begin)), end = min(int64_t(all.end), int64_t(begin) + chunk);
+    const bool alone = all.end - all.begin <= chunk;
+    if (begin >= end && share > 0) return;
+    const bool two = RT > 1 && rows > 16;
+
+    // this lane's rows: one of each block of 16
+    int pos[RT], first[RT];
+    x8 q[RT][2 * C];
+#pragma unroll
+    for (int rb = 0; rb < RT; rb++) {
+        const int r = 16 * rb + col, i = r / a.G;
+        const bool there = r < rows;
+        pos[rb] = there ? s.pos0 + i : -1;
+        first[rb] = a.window ? pos[rb] - a.window : -1;              // keys after this one
+        const T *qr = static_cast<const T *>(a.q) + int64_t(s.start + (there ? i : 0)) * a.qdt + int64_t(h * a.G + (there ? r - i * a.G : 0)) * a.qdh;
+#pragma unroll
+        for (int c = 0; c < C; c++)
+#pragma unroll
+            for (int e = 0; e < 2; e++) q[rb][2 * c + e] = load_x8(qr + 64 * c + 16 * g + 8 * e);
+    }
+    float m[RT], l[RT];
+    f32x4 o[RT][C][4];
+#pragma unroll
+    for (int rb = 0; rb < RT; rb++) {
+        m[rb] = NEG;
+        l[rb] = 0.0f;
+#pragma unroll
+        for (int c = 0; c < C; c++)
+#pragma unroll
+            for (int k = 0; k < 4; k++) o[rb][c][k] = f32x4{0, 0, 0, 0};
+    }
+
+    // wave w takes the 32-key units w, w + 4, ... of the share
+    const int units = (end - begin + 31) / 32;
+    int tiles = -1;
+    for (int u = wv, it = 0; u < units; u += 4, it++) {
+        if ((it & 31) == 0) {                                        // the tiles of this unit and the 31 behind it
+            const int k16 = begin / 16 + 2 * (u + 4 * (lane >> 1)) + (lane & 1);
+            tiles = 16 * k16 < end ? cache_tile(a, b, h, k16) : -1;
+        }
+        const int key0 = begin + 32 * u;
+        u32x4 kc[2][C], vc[2][C];
+        f32x4 ks[2], vs[2];
+        bool there[2];
+#pragma unroll
+        for (int j = 0; j < 2; j++) {
+            const int t = __builtin_amdgcn_readlane(tiles, 2 * (it & 31) + j);
+            there[j] = t >= 0;
+            const uint8_t *p = a.cache + int64_t(max(t, 0)) * TILE;  // a tile that is not there: any, and masked
+#pragma unroll
+            for (int c = 0; c < C; c++) {
+                kc[j][c] = *reinterpret_cast<const u32x4 *>(p + c * 1024 + lane * 16);
+                vc[j][c] = *reinterpret_cast<const u32x4 *>(p + 16 * D + c * 1024 + lane * 16);
+            }
+            ks[j] = *reinterpret_cast<const f32x4 *>(p + 32 * D + 16 * g);
+            vs[j] = *reinterpret_cast<const f32x4 *>(p + 32 * D + 64 + 16 * g);
+        }
+        f32x4 sc[RT][2];
+#pragma unroll
+        for (int j = 0; j < 2; j++) {
+#pragma unroll
+            for (int rb = 0; rb < RT; rb++) sc[rb][j] = f32x4{0, 0, 0, 0};
+#pragma unroll
+            for (int c = 0; c < C; c++)
+#pragma unroll
+                for (int e = 0; e < 2; e++) {
+                    const x8 k = codes8<T>(kc[j][c][2 * e], kc[j][c][2 * e + 1]);
+#pragma unroll
+                    for (int rb = 0; rb < RT; rb++)
+                        if (rb == 0 || two) sc[rb][j] = Half<T>::mfma16(k, q[rb][2 * c + e], sc[rb][j]);
+                }
+        }
+        x8 p8[RT];
+#pragma unroll
+        for (int rb = 0; rb < RT; rb++) {
+            if (rb > 0 && !two) continue;
+            float t[2][4], top = NEG, low = NEG;
+            bool seen[2][4];
+#pragma unroll
+            for (int j = 0; j < 2; j++)
+#pragma unroll
+                for (int i = 0; i < 4; i++) {
+                    const int key = key0 + 16 * j + 4 * g + i;
+                    seen[j][i] = there[j] && key <= pos[rb] && key > first[rb];
+                    t[j][i] = seen[j][i] ? sc[rb][j][i] * (ks[j][i] * a.scale) : NEG;
+                    top = fmaxf(top, t[j][i]);
+                    if (Half<T>::NARROW) low = fmaxf(low, seen[j][i] ? t[j][i] + __builtin_amdgcn_logf(vs[j][i]) : NEG);
+                }
+            float want = Half<T>::NARROW ? fmaxf(low - kNarrowTop, top - kNarrowSum) : top;
+            want = fmaxf(want, __shfl_xor(want, 16));
+            want = fmaxf(want, __shfl_xor(want, 32));
+            if (__any(want > m[rb] + kSlack || (m[rb] == NEG && want > NEG))) {
+                const float to = fmaxf(m[rb], want), f = to == NEG ? 1.0f : __builtin_amdgcn_exp2f(m[rb] - to);
+                m[rb] = to;
+                l[rb] *= f;
+#pragma unroll
+                for (int c = 0; c < C; c++)
+#pragma unroll
+                    for (int k = 0; k < 4; k++) o[rb][c][k] *= f;
+            }
+            const float ref = m[rb] == NEG ? 0.0f : m[rb];
+            T w[8];
+#pragma unroll
+            for (int j = 0; j < 2; j++)
+#pragma unroll
+                for (int i = 0; i < 4; i++) {
+                    const float p = __builtin_amdgcn_exp2f(t[j][i] - ref);
+                    l[rb] += p;
+                    w[4 * j + i] = T(seen[j][i] ? p * vs[j][i] : 0.0f);
+                }
+            __builtin_memcpy(&p8[rb], w, 16);
+        }
+#pragma unroll
+        for (int c = 0; c < C; c++)
+#pragma unroll
+            for (int k = 0; k < 4; k++) {
+                const x8 v = codes8<T>(vc[0][c][k], vc[1][c][k]);
+#pragma unroll
+                for (int rb = 0; rb < RT; rb++)
+                    if (rb == 0 || two) o[rb][c][k] = Half<T>::mfma16(v, p8[rb], o[rb][c][k]);
+            }
+    }
+
+    // the four waves' shares, then the result, 64 columns at a time
+#pragma unroll
+    for (int rb = 0; rb < RT; rb++) {
+        l[rb] += __shfl_xor(l[rb], 16);
+        l[rb] += __shfl_xor(l[rb], 32);
+        if (g == 0) {
+            S_m[wv][16 * rb + col] = m[rb];
+            S_l[wv][16 * rb + col] = l[rb];
+        }
+    }
+    __syncthreads();
+    float f[RT];
+#pragma unroll
+    for (int rb = 0; rb < RT; rb++) {
+        const int r = 16 * rb + col;
+        const float to = fmaxf(fmaxf(S_m[0][r], S_m[1][r]), fmaxf(S_m[2][r], S_m[3][r]));
+        f[rb] = m[rb] == NEG ? 0.0f : __builtin_amdgcn_exp2f(m[rb] - to);
+    }
+#pragma unroll
+    for (int c = 0; c < C; c++) {
+        if (c) __syncthreads();
+#pragma unroll
+        for (int rb = 0; rb < RT; rb++)
+#pragma unroll
+            for (int i = 0; i < 4; i++) {                            // register i of o[..][k]: column 16 g + 4 i + k
+                const f32x4 v = {o[rb][c][0][i] * f[rb], o[rb][c][1][i] * f[rb], o[rb][c][2][i] * f[rb], o[rb][c][3][i] * f[rb]};
+                *reinterpret_cast<f32x4 *>(&S_o[wv][16 * rb + col][16 * g + 4 * i]) = v;
+            }
+        __syncthreads();
+#pragma unroll
+        for (int x = threadIdx.x; x < R * 16; x += 256) {
+            const int r = x / 16, d = 4 * (x % 16);
+            if (r >= rows) continue;
+            f32x4 v = {0, 0, 0, 0};
+            float to = NEG, sum = 0.0f;
+#pragma unroll
+            for (int w = 0; w < 4; w++) {
+                v += *reinterpret_cast<const f32x4 *>(&S_o[w][r][d]);
+                to = fmaxf(to, S_m[w][r]);
+            }
+#pragma unroll
+            for (int w = 0; w < 4; w++) sum += S_m[w][r] == NEG ? S_l[w][r] : S_l[w][r] * __builtin_amdgcn_exp2f(S_m[w][r] - to);
+            if (alone) {
+                const int i = r / a.G;
+                O *out = static_cast<O *>(a.out) + int64_t(s.start + i) * a.odt + int64_t(h * a.G + r - i * a.G) * a.odh;
+                store4(out + 64 * c + d, sum == 0.0f ? f32x4{0, 0, 0, 0} : v * (1.0f / sum));
+            } else {
+                const int64_t slot = ((int64_t(b) * a.Hkv + h) * a.split + share) * R + r;
+                *reinterpret_cast<f32x4 *>(a.part + slot * D + 64 * c + d) = v;
+                if (c == 0 && d == 0) {
+                    float *ml = a.part + int64_t(a.units) * a.Hkv * a.split * R * D + 2 * slot;
+                    ml[0] = to;
+                    ml[1] = sum;
+                }
+            }
+        }
+    }
+}
+
+// --- tile kernel ------------------------------------------------------------
+
+// The sequence and its tile of BM rows that tile number `tile` of the launch
+// is; false past the last.  Only sequences of many rows have tiles.
+template <int BM>
+__device__ __forceinline__ bool find_tile(const AttnArgs &a, int tile, int &b, int &in, int &of) {
+    const int lane = threadIdx.x & 63;
+    int before = 0;
+    for (int b0 = 0; b0 < a.B; b0 += 64) {
+        int n = 0;
+        if (b0 + lane < a.B) {
+            const Seq s = sequence(a, b0 + lane);
+            if (!has_few_rows(a, s.n)) n = int((int64_t(s.n) * a.G + BM - 1) / BM);
+        }
+        const int upto = scan_sum(n);
+        const unsigned long long hit = __ballot(before + upto > tile);
+        if (hit) {
+            const int i = __builtin_ctzll(hit);
+            b = b0 + i;
+            of = __builtin_amdgcn_readlane(n, i);
+            in = tile - before - (__builtin_amdgcn_readlane(upto, i) - of);
+            return true;
+        }
+        before += __builtin_amdgcn_readlane(upto, 63);
+    }
+    return false;
+}
+
+// Keys of each share of a tile.
+__device__ __forceinline__ int tile_chunk(const AttnArgs &a, const Range &r) {
+    const int even = (r.end - r.begin + a.split - 1) / a.split;
+    return max((even + 63) & ~63, kAttnTileChunk);
+}
+
+template <typename T, typename O, int D, int WAVES>
+__global__ __launch_bounds__(64 * WAVES) void k_attn_tile(AttnArgs a) {
+    typedef typename Half<T>::x8 x8;
+    constexpr int THREADS = 64 * WAVES, BM = 32 * WAVES, TILE = int(kv_tile_bytes(D));
+    constexpr int KS = D / 16, DT = D / 32;              // steps of the first product, column tiles of the second
+    constexpr int LOADS = 8 * D / THREADS;               // 16-byte loads of a lane for 64 keys and values
+    constexpr int BUF = 2 * 64 * D * 2;                  // K then V, 16 bits each
+    constexpr float NEG = -__builtin_inff();
+    static_assert(8 * D % THREADS == 0, "whole loads");
+    __shared__ __align__(16) uint8_t S[2][BUF];
+    __shared__ __align__(16) float S_ks[2][64], S_vs[2][64], S_lv[2][64];
+    const int tid = threadIdx.x, lane = tid & 63, wv = __builtin_amdgcn_readfirstlane(tid >> 6), col = lane & 31, hf = lane >> 5;
+    const int h = blockIdx.x % a.Hkv, rest = blockIdx.x / a.Hkv, share = rest / a.units;
+    int b, in, of;
+    if (!find_tile<BM>(a, rest % a.units, b, in, of)) return;
+    b = __builtin_amdgcn_readfirstlane(b);
+    in = of - 1 - __builtin_amdgcn_readfirstlane(in);    // the rows with the most keys first
+    const Seq s = sequence(a, b);
+    const int rows = s.n * a.G, row0 = in * BM;
+    const Range all(a, s, row0 / a.G, (min(row0 + BM, rows) - 1) / a.G);
+    const int chunk = tile_chunk(a, all);
+    const int begin = all.begin + min(int64_t(share) * chunk, int64_t(all.end - all.begin)), end = min(int64_t(all.end), int64_t(begin) + chunk);
+    const bool alone = all.end - all.begin <= chunk;
+    if (begin >= end && share > 0) return;
+
+    // this lane's row
+    const int r = row0 + 32 * wv + col, tok = r / a.G;
+    const bool there = r < rows;
+    const int pos = there ? s.pos0 + tok : -1, first = a.window ? pos - a.window : -1;
+    x8 q[KS];
+    {
+        const T *qr = static_cast<const T *>(a.q) + int64_t(s.start + (there ? tok : 0)) * a.qdt + int64_t(h * a.G + (there ? r - tok * a.G : 0)) * a.qdh;
+#pragma unroll
+        for (int k = 0; k < KS; k++) q[k] = load_x8(qr + 16 * k + 8 * hf);
+    }
+    // what the wave's rows see: all of keys (lo_all, hi_all], something of (lo_any, hi_any]
+    const int wr0 = row0 + 32 * wv, wr1 = min(wr0 + 32, rows) - 1;
+    const bool active = wr0 < rows;
+    const int p_lo = s.pos0 + wr0 / a.G, p_hi = s.pos0 + wr1 / a.G;
+    const int hi_any = p_hi, hi_all = p_lo;
+    const int lo_any = a.window ? p_lo - a.window : -1, lo_all = a.window ? p_hi - a.window : -1;
+
+    float m = NEG, l = 0.0f;
+    f32x16 o[DT];
+#pragma unroll
+    for (int d = 0; d < DT; d++)
+#pragma unroll
+        for (int i = 0; i < 16; i++) o[d][i] = 0.0f;
+
+    const int steps = (end - begin + 63) / 64;
+    u32x4 st[LOADS];
+    float st_scale = 0.0f;
+    int tiles = -1;                                       // of 16 steps: lane 4 i + j holds 16-key tile j of step i
+    auto look_up = [&](int step) {
+        const int k16 = begin / 16 + 4 * step + lane;
+        tiles = 16 * k16 < end ? cache_tile(a, b, h, k16) : -1;
+    };
+    int valid[2];                                         // of the two buffers: which of their four tiles are there
+    auto load = [&](int step) {
+        if ((step & 15) == 0) look_up(step);
+#pragma unroll
+        for (int i = 0; i < LOADS; i++) {
+            const int c = i * THREADS + wv * 64, part = c / D, at = c % D;      // parts: K and V of each 16-key tile
+            const int t = max(__builtin_amdgcn_readlane(tiles, 4 * (step & 15) + part / 2), 0);
+            st[i] = *reinterpret_cast<const u32x4 *>(a.cache + int64_t(t) * TILE + (part & 1) * 16 * D + (at + lane) * 16);
+        }
+        if (tid < 128) {                                  // wave 0: key scales; wave 1: value scales
+            const int t = __shfl(tiles, 4 * (step & 15) + (lane >> 4));
+            st_scale = t >= 0 && begin + 64 * step + lane < end
+                           ? reinterpret_cast<const float *>(a.cache + int64_t(t) * TILE + 32 * D)[16 * wv + (lane & 15)]
+                           : 0.0f;
+        }
+    };
+    auto store = [&](int step) {
+        const int buf = step & 1;
+        const unsigned long long ok = __ballot(tiles >= 0);
+        valid[buf] = int(ok >> (4 * (step & 15))) & 15;
+#pragma unroll
+        for (int i = 0; i < LOADS; i++) {
+            const int c = i * THREADS + wv * 64, part = c / D, at = c % D, t16 = part / 2;
+            uint32_t w[4][2];
+#pragma unroll
+            for (int k = 0; k < 4; k++) Half<T>::codes(st[i][k], w[k]);
+            if (!(part & 1)) {
+                // K: lane = (chunk of 16 d, token): fragment (32 keys, 16 d): [half of d][key][8 d]
+                const int ch = (at + lane) >> 4, key = 16 * (t16 & 1) + (lane & 15);
+                uint8_t *p = S[buf] + ((t16 >> 1) * KS + ch) * 1024 + key * 16;
+                *reinterpret_cast<u32x4 *>(p) = u32x4{w[0][0], w[0][1], w[1][0], w[1][1]};
+                *reinterpret_cast<u32x4 *>(p + 512) = u32x4{w[2][0], w[2][1], w[3][0], w[3][1]};
+            } else {
+                // V: lane = (four tokens g, four d): fragment (16 keys, 32 d): [g & 1][d][g >> 1][4 tokens]
+                const int v64 = at / 64, gg = lane >> 4;
+                uint8_t *p = S[buf] + 128 * D + (t16 * DT + 2 * v64) * 1024 + (gg & 1) * 512 + (lane & 15) * 16 + (gg >> 1) * 8;
+#pragma unroll
+                for (int k = 0; k < 4; k++) *reinterpret_cast<uint2 *>(p + (k >> 1) * 1024 + (k & 1) * 256) = make_uint2(w[k][0], w[k][1]);
+            }
+        }
+        if (wv == 0) S_ks[buf][lane] = st_scale * a.scale;
+        if (wv == 1) {
+            S_vs[buf][lane] = st_scale;
+            if (Half<T>::NARROW) S_lv[buf][lane] = __builtin_amdgcn_logf(st_scale);
+        }
+    };
+    if (steps > 0) {
+        load(0);
+        store(0);
+        if (steps > 1) load(1);
+    }
+    for (int step = 0; step < steps; step++) {
+        const int buf = step & 1, key0 = begin + 64 * step;
+        __syncthreads();
+        if (step + 1 < steps) {
+            store(step + 1);
+            if (step + 2 < steps) load(step + 2);
+        }
+        if (!active || key0 > hi_any || key0 + 63 <= lo_any) continue;
+        const uint8_t *K = S[buf], *V = K + 128 * D;
+        f32x16 sc[2];
+#pragma unroll
+        for (int j = 0; j < 2; j++) {
+#pragma unroll
+            for (int i = 0; i < 16; i++) sc[j][i] = 0.0f;
+#pragma unroll
+            for (int k = 0; k < KS; k++)
+                sc[j] = Half<T>::mfma32(*reinterpret_cast<const x8 *>(K + (j * KS + k) * 1024 + lane * 16), q[k], sc[j]);
+        }
+        const bool whole = valid[buf] == 15 && key0 + 63 <= hi_all && key0 > lo_all;
+        // register i of half j: key 32 j + 8 (i / 4) + 4 hf + i % 4
+        float top = NEG, low = NEG;
+#pragma unroll
+        for (int j = 0; j < 2; j++)
+#pragma unroll
+            for (int x = 0; x < 4; x++) {
+                const int at = 32 * j + 8 * x + 4 * hf;
+                const f32x4 ks = *reinterpret_cast<const f32x4 *>(&S_ks[buf][at]);
+#pragma unroll
+                for (int y = 0; y < 4; y++) sc[j][4 * x + y] *= ks[y];
+                if (!whole) {
+#pragma unroll
+                    for (int y = 0; y < 4; y++) {
+                        const int key = key0 + at + y;
+                        const bool seen = (valid[buf] >> (2 * j + x / 2) & 1) && key <= pos && key > first;
+                        if (!seen) sc[j][4 * x + y] = NEG;
+                    }
+                }
+                f32x4 lv = {0, 0, 0, 0};
+                if (Half<T>::NARROW) lv = *reinterpret_cast<const f32x4 *>(&S_lv[buf][at]);
+#pragma unroll
+                for (int y = 0; y < 4; y++) {
+                    top = fmaxf(top, sc[j][4 * x + y]);
+                    if (Half<T>::NARROW) {
+                        // a masked score is -inf and its sum with a scale that is 0, infinite or NaN must not count
+                        const float u = sc[j][4 * x + y] + lv[y];
+                        low = fmaxf(low, sc[j][4 * x + y] == NEG ? NEG : u);
+                    }
+                }
+            }
+        float want = Half<T>::NARROW ? fmaxf(low - kNarrowTop, top - kNarrowSum) : top;
+        want = fmaxf(want, __shfl_xor(want, 32));
+        if (__any(want > m + kSlack || (m == NEG && want > NEG))) {
+            const float to = fmaxf(m, want), f = to == NEG ? 1.0f : __builtin_amdgcn_exp2f(m - to);
+            m = to;
+            l *= f;
+#pragma unroll
+            for (int d = 0; d < DT; d++)
+#pragma unroll
+                for (int i = 0; i < 16; i++) o[d][i] *= f;
+        }
+        const float ref = m == NEG ? 0.0f : m;
+#pragma unroll
+        for (int c = 0; c < 4; c++) {                     // 16 keys: registers 8 (c % 2) .. + 7 of half c / 2
+            T w[8];
+#pragma unroll
+            for (int x = 0; x < 2; x++) {
+                const f32x4 vs = *reinterpret_cast<const f32x4 *>(&S_vs[buf][16 * c + 8 * x + 4 * hf]);
+#pragma unroll
+                for (int y = 0; y < 4; y++) {
+                    const float t = sc[c / 2][8 * (c % 2) + 4 * x + y], p = __builtin_amdgcn_exp2f(t - ref);
+                    l += p;
+                    w[4 * x + y] = T(!whole && t == NEG ? 0.0f : p * vs[y]);
+                }
+            }
+            x8 p8;
+            __builtin_memcpy(&p8, w, 16);
+#pragma unroll
+            for (int d = 0; d < DT; d++)
+                o[d] = Half<T>::mfma32(*reinterpret_cast<const x8 *>(V + (c * DT + d) * 1024 + lane * 16), p8, o[d]);
+        }
+    }
+    l += __shfl_xor(l, 32);
+    if (!there) return;
+    // register i of o[2 v + p]: column 64 v + 32 (i / 4 % 2) + 16 hf + 4 (i % 4) + 2 p + i / 8
+    const float inv = alone ? (l == 0.0f ? 0.0f : 1.0f / l) : 1.0f;
+    const int64_t slot = ((int64_t(rest % a.units) * a.Hkv + h) * a.split + share) * BM + 32 * wv + col;
+    O *out = static_cast<O *>(a.out) + int64_t(s.start + tok) * a.odt + int64_t(h * a.G + r - tok * a.G) * a.odh;
+#pragma unroll
+    for (int v = 0; v < D / 64; v++)
+#pragma unroll
+        for (int x = 0; x < 2; x++)
+#pragma unroll
+            for (int y = 0; y < 4; y++) {
+                const int i = 4 * x + y, d = 64 * v + 32 * x + 16 * hf + 4 * y;
+                const f32x4 w = {o[2 * v][i] * inv, o[2 * v][i + 8] * inv, o[2 * v + 1][i] * inv, o[2 * v + 1][i + 8] * inv};
+                if (alone)
+                    store4(out + d, l == 0.0f ? f32x4{0, 0, 0, 0} : w);
+                else
+                    *reinterpret_cast<f32x4 *>(a.part + slot * D + d) = w;
+            }
+    if (!alone && hf == 0) {
+        float *ml = a.part + int64_t(a.units) * a.Hkv * a.split * BM * D + 2 * slot;
+        ml[0] = m;
+        ml[1] = l;
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Joins shares: D / 4 lanes a row, the rows of one (sequence, head) or (tile,
+// head) a workgroup.  Rows whose keys were not split have been written.
+// ---------------------------------------------------------------------------
+template <typename O, int D, int BM, bool TILES>
+__global__ __launch_bounds__(256) void k_attn_join(AttnArgs a) {
+    constexpr int LANES = D / 4, ROWS = 256 / LANES, GROUPS = (BM + ROWS - 1) / ROWS;
+    constexpr float NEG = -__builtin_inff();
+    const int group = blockIdx.x % GROUPS, unit = blockIdx.x / GROUPS, h = unit % a.Hkv;
+    int b = unit / a.Hkv, in = 0, of = 1;
+    if (TILES) {
+        if (!find_tile<BM>(a, unit / a.Hkv, b, in, of)) return;
+        b = __builtin_amdgcn_readfirstlane(b);
+        in = of - 1 - __builtin_amdgcn_readfirstlane(in);
+    }
+    const Seq s = sequence(a, b);
+    if (s.n == 0 || has_few_rows(a, s.n) == TILES) return;
+    const int rows = s.n * a.G, row0 = in * BM;
+    const Range all(a, s, row0 / a.G, (min(row0 + BM, rows) - 1) / a.G);
+    const int chunk = TILES ? tile_chunk(a, all) : few_chunk(a);
+    const int shares = (all.end - all.begin + chunk - 1) / chunk;
+    const int r = group * ROWS + threadIdx.x / LANES, d = 4 * (threadIdx.x % LANES);
+    if (shares <= 1 || r >= BM || row0 + r >= rows) return;
+    const int64_t slot0 = int64_t(unit) * a.split * BM + r;
+    const float *ml = a.part + int64_t(a.units) * a.Hkv * a.split * BM * D;
+    float to = NEG;
+    for (int k = 0; k < shares; k++) to = fmaxf(to, ml[2 * (slot0 + int64_t(k) * BM)]);
+    f32x4 v = {0, 0, 0, 0};
+    float sum = 0.0f;
+    for (int k = 0; k < shares; k++) {
+        const int64_t slot = slot0 + int64_t(k) * BM;
+        const float m = ml[2 * slot], f = m == NEG ? 0.0f : __builtin_amdgcn_exp2f(m - to);
+        // a share that saw no finite maximum adds nothing, unless it holds a NaN
+        sum += m == NEG ? ml[2 * slot + 1] : ml[2 * slot + 1] * f;
+        v += *reinterpret_cast<const f32x4 *>(a.part + slot * D + d) * f;
+    }
+    const int i = (row0 + r) / a.G;
+    O *out = static_cast<O *>(a.out) + int64_t(s.start + i) * a.odt + int64_t(h * a.G + row0 + r - i * a.G) * a.odh;
+    store4(out + d, sum == 0.0f ? f32x4{0, 0, 0, 0} : v * (1.0f / sum));
+}
+
+// ---------------------------------------------------------------------------
+// Launchers
+// ---------------------------------------------------------------------------
+template <typename T, typename O, int D>
+static hipError_t launch_dim(const AttnPlan &p, AttnArgs a, void *workspace, hipStream_t stream) {
+    uint8_t *ws = static_cast<uint8_t *>(workspace);
+    if (p.few_tiles) {
+        a.split = p.few_split;
+        a.units = a.B;
+        a.part = reinterpret_cast<float *>(ws);
+        const dim3 grid{unsigned(p.few_grid)};
+        const unsigned units = unsigned(a.B) * unsigned(a.Hkv);
+        constexpr unsigned ROWS = 1024 / D;
+        if (p.few_tiles == 1) {
+            k_attn_rows<T, O, D, 1><<<grid, 256, 0, stream>>>(a);
+            if (a.split > 1) k_attn_join<O, D, 16, false><<<dim3(units * ((16 + ROWS - 1) / ROWS)), 256, 0, stream>>>(a);
+        } else {
+            k_attn_rows<T, O, D, 2><<<grid, 256, 0, stream>>>(a);
+            if (a.split > 1) k_attn_join<O, D, 32, false><<<dim3(units * ((32 + ROWS - 1) / ROWS)), 256, 0, stream>>>(a);
+        }
+    }
+    if (p.tile_rows) {
+        constexpr int WAVES = D == 256 ? 4 : 8, BM = 32 * WAVES;
+        a.split = p.tile_split;
+        a.units = int(p.tiles);
+        a.part = reinterpret_cast<float *>(ws + p.few_bytes);
+        k_attn_tile<T, O, D, WAVES><<<dim3(unsigned(p.tile_grid)), 64 * WAVES, 0, stream>>>(a);
+        if (a.split > 1)
+            k_attn_join<O, D, BM, true><<<dim3(unsigned(p.tiles) * unsigned(a.Hkv) * (BM * D / 1024)), 256, 0, stream>>>(a);
+    }
+    return hipGetLastError();
+}
+
+template <typename T, typename O>
+static hipError_t launch_out(const AttnPlan &p, const AttnArgs &a, int D, void *workspace, hipStream_t stream) {
+    if (D == 64) return launch_dim<T, O, 64>(p, a, workspace, stream);
+    if (D == 128) return launch_dim<T, O, 128>(p, a, workspace, stream);
+    return launch_dim<T, O, 256>(p, a, workspace, stream);
+}
+
+hipError_t launch_attention(const AttnPlan &p, int type, const void *q, int64_t qdt, int64_t qdh, const void *cache,
+                            int64_t n_pages, int page, const int32_t *table, int64_t max_pages, const int32_t *lens,
+                            const int32_t *offsets, int64_t B, int64_t T, int64_t max_q, int Hq, int Hkv, int D, float scale,
+                            int window, int out_type, void *out, int64_t odt, int64_t odh, void *workspace,
+                            hipStream_t stream) {
+    AttnArgs a{};
+    a.q = q; a.qdt = qdt; a.qdh = qdh;
+    a.cache = static_cast<const uint8_t *>(cache);
+    a.table = table; a.lens = lens; a.offsets = offsets;
+    a.out = out; a.odt = odt; a.odh = odh;
+    a.n_pages = n_pages; a.max_pages = max_pages;
+    a.page_shift = __builtin_ctz(unsigned(page));
+    a.Hq = Hq; a.Hkv = Hkv; a.G = Hq / Hkv;
+    a.T = int(T); a.B = int(B); a.max_q = int(max_q < T ? max_q : T); a.window = window;
+    a.scale = float(double(scale) * 1.4426950408889634074);
+    a.target = p.target;
+    if (type == TYPE_BF16)
+        return out_type == TYPE_F32 ? launch_out<__bf16, float>(p, a, D, workspace, stream)
+                                    : launch_out<__bf16, __bf16>(p, a, D, workspace, stream);
+    return out_type == TYPE_F32 ? launch_out<_Float16, float>(p, a, D, workspace, stream)
+                                : launch_out<_Float16, _Float16>(p, a, D, workspace, stream);
+}
+
+}  // namespace mmq

@@ -18,7 +18,9 @@
 
 #include <type_traits>
 
+#include "i8_codes.hpp"
 #include "i8_plan.hpp"
+#include "wave_scan.hpp"
 
 namespace mmq {
 
@@ -150,26 +152,9 @@ __global__ __launch_bounds__(THREADS < 256 ? 256 : THREADS) void k_quantize_i8(
 #pragma unroll
         for (int w = 0; w < THREADS / 64; w++) am = max(am, part[w]);
     }
-    const bool finite = am < 0x7f800000u;
-    const float d = __uint_as_float(am) / 127.0f;                        // correctly rounded
-    float id = (finite && d != 0.0f) ? 1.0f / d : 0.0f;
-    if (__builtin_isinf(id)) id = 0.0f;
-    // |x * id| <= 127 (1 + 2^-21), so the rounded code needs no clamp
+    const RowCode code(am);
     auto store = [&](int c, const float (&w)[kChunk]) {
-        uint32_t pk[2];
-#pragma unroll
-        for (int g = 0; g < 2; g++) {
-            int k[4];
-#pragma unroll
-            for (int i = 0; i < 4; i++) {
-                // half away from zero: adding the number below 1/2 carries exactly the halves and what is above them
-                const float y = w[4 * g + i] * id;
-                k[i] = finite ? int(y + __builtin_copysignf(0x1.fffffep-2f, y)) : 0;
-            }
-            const uint32_t lo = __builtin_amdgcn_perm(k[1], k[0], 0x0c0c0400u), hi = __builtin_amdgcn_perm(k[3], k[2], 0x0c0c0400u);
-            pk[g] = __builtin_amdgcn_perm(hi, lo, 0x05040100u);
-        }
-        *reinterpret_cast<uint2 *>(q + row * ldq + kChunk * c) = make_uint2(pk[0], pk[1]);
+        *reinterpret_cast<uint2 *>(q + row * ldq + kChunk * c) = encode8(w, code);
     };
 #pragma unroll
     for (int i = 0; i < CH; i++)
@@ -179,41 +164,12 @@ __global__ __launch_bounds__(THREADS < 256 ? 256 : THREADS) void k_quantize_i8(
         values(c, w);
         store(c, w);
     }
-    if (tid == 0) scale[row] = finite ? d : __uint_as_float(0x7fc00000u);
+    if (tid == 0) scale[row] = code.scale();
 }
 
 // ---------------------------------------------------------------------------
 // GEMM
 // ---------------------------------------------------------------------------
-
-// Inclusive scans of numbers >= 0 over the lanes of a wave, by DPP: shifts
-// within the rows of 16 lanes, then each row's last lane to the rows behind.
-template <int CTRL, int ROWS>
-__device__ __forceinline__ int dpp_or_0(int v) {
-    return __builtin_amdgcn_update_dpp(0, v, CTRL, ROWS, 0xf, false);
-}
-__device__ __forceinline__ int scan_sum(int v) {
-    v += dpp_or_0<0x111, 0xf>(v);      // row_shr:1
-    v += dpp_or_0<0x112, 0xf>(v);
-    v += dpp_or_0<0x114, 0xf>(v);
-    v += dpp_or_0<0x118, 0xf>(v);
-    v += dpp_or_0<0x142, 0xa>(v);      // row_bcast:15 into rows 1 and 3
-    v += dpp_or_0<0x143, 0xc>(v);      // row_bcast:31 into rows 2 and 3
-    return v;
-}
-__device__ __forceinline__ int scan_max(int v) {
-    v = max(v, dpp_or_0<0x111, 0xf>(v));
-    v = max(v, dpp_or_0<0x112, 0xf>(v));
-    v = max(v, dpp_or_0<0x114, 0xf>(v));
-    v = max(v, dpp_or_0<0x118, 0xf>(v));
-    v = max(v, dpp_or_0<0x142, 0xa>(v));
-    v = max(v, dpp_or_0<0x143, 0xc>(v));
-    return v;
-}
-// The lane before's v; `first` in lane 0.
-__device__ __forceinline__ int lane_before(int v, int first) {
-    return __builtin_amdgcn_update_dpp(first, v, 0x138, 0xf, 0xf, false);      // wave_shr:1
-}
 
 // The group that tile `tile` of a grouped launch belongs to: its expert and
 // its rows [row, end).  A wave scans the experts 64 at a time; false past the

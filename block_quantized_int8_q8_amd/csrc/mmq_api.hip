@@ -18,11 +18,15 @@
 #include <utility>
 
 #include "../../include/mmq.h"
+#include "attn_plan.hpp"
 #include "i8_plan.hpp"
 #include "mmq_plan.hpp"
 
 static_assert(mmq::TYPE_F32 == MMQ_TYPE_F32 && mmq::TYPE_BF16 == MMQ_TYPE_BF16 && mmq::TYPE_F16 == MMQ_TYPE_F16 &&
                   mmq::kI8MaxK == MMQ_I8_MAX_K,
+              "header and library disagree");
+static_assert(mmq::ROPE_PLAIN == MMQ_ROPE_PLAIN && mmq::ROPE_LINEAR == MMQ_ROPE_LINEAR && mmq::ROPE_BANDS == MMQ_ROPE_BANDS &&
+                  mmq::ROPE_YARN == MMQ_ROPE_YARN && MMQ_ROPE_HALF == 0 && MMQ_ROPE_INTERLEAVED == 1,
               "header and library disagree");
 static_assert(mmq::kNoAllocMaxRouted == MMQ_MOE_NOALLOC_MAX_ROUTED, "header and library disagree");
 
@@ -42,6 +46,21 @@ hipError_t launch_gemm_i8(const I8Plan &p, int type, const void *x, int64_t ldx,
                           const int32_t *rows, const int32_t *offsets, int experts, const void *w, int64_t ldw,
                           const float *ws, const float *bias, void *out, int64_t ldo, int64_t M, int64_t N, int64_t K,
                           hipStream_t stream);
+hipError_t launch_rope(int type, const void *x, int64_t ldt, int64_t ldh, int out_type, void *out, int64_t odt, int64_t odh,
+                       const int32_t *positions, const double *freqs, int rot, int layout, double mscale, int inverse,
+                       int64_t T, int H, int D, int cu_count, hipStream_t stream);
+hipError_t launch_kv_write(int type, const void *k, int64_t kdt, int64_t kdh, const void *v, int64_t vdt, int64_t vdh,
+                           const int32_t *positions, const double *freqs, int rot, int layout, double mscale,
+                           const int32_t *slots, int64_t T, void *cache, int64_t n_pages, int page, int H, int D, int cu_count,
+                           hipStream_t stream);
+hipError_t launch_kv_read(int type, const void *cache, int64_t n_pages, int page, int H, int D, const int32_t *slots, int64_t T,
+                          void *k, int64_t kdt, int64_t kdh, void *v, int64_t vdt, int64_t vdh, int cu_count,
+                          hipStream_t stream);
+hipError_t launch_attention(const AttnPlan &p, int type, const void *q, int64_t qdt, int64_t qdh, const void *cache,
+                            int64_t n_pages, int page, const int32_t *table, int64_t max_pages, const int32_t *lens,
+                            const int32_t *offsets, int64_t B, int64_t T, int64_t max_q, int Hq, int Hkv, int D, float scale,
+                            int window, int out_type, void *out, int64_t odt, int64_t odh, void *workspace,
+                            hipStream_t stream);
 }  // namespace mmq
 
 namespace {
@@ -610,6 +629,186 @@ int mmq_plan_i8(int64_t M, int64_t N, int64_t K, int n_experts, int cu_count, ch
             std::snprintf(buf, size_t(len), "%s", bad ? bad : why);
     }
     return ok ? 1 : 0;
+}
+
+}  // extern "C"
+
+namespace {
+
+// Device of a call of the operators below: its CU count, or 0 after a refusal.
+int gfx950_cus() {
+    DeviceLimits L;
+    if (!current_limits(&L)) return 0;
+    if (!L.is_gfx950) return refuse("device is %s; this library is built for gfx950 only", L.arch);
+    (void)hipGetLastError();
+    return L.cu_count;
+}
+
+int launched(const char *name, hipError_t e) {
+    if (e != hipSuccess) return refuse("%s launch failed: %s", name, hipGetErrorString(e));
+    return 1;
+}
+
+// The rotation of a call, if it has one: nullptr when it is fine.
+const char *check_rotation(const int32_t *positions, const double *freqs, int D, int rot, int layout, double mscale) {
+    if (const char *bad = mmq::check_rope(D, rot, layout)) return bad;
+    if (!positions || !freqs) return "null pointer argument";
+    if (!aligned(positions, 4) || !aligned(freqs, 8)) return "positions must be 4-byte and frequencies 8-byte aligned";
+    if (!(mscale - mscale == 0.0)) return "mscale must be finite";
+    return nullptr;
+}
+
+}  // namespace
+
+extern "C" {
+
+int mmq_rope_frequencies(int scaling, int rot, double base, double factor, double low, double high, int64_t original,
+                         double *freqs, double *mscale) {
+    g_err[0] = '\0';
+    if (const char *bad = mmq::check_frequencies(scaling, rot, base, factor, low, high, original))
+        return refuse("rope frequencies: %s", bad);
+    if (!freqs || !mscale) return refuse("null pointer argument");
+    mmq::rope_frequencies(scaling, rot, base, factor, low, high, original, freqs, mscale);
+    return 1;
+}
+
+int mmq_rope(int type, const void *x, int64_t ldt, int64_t ldh, int out_type, void *out, int64_t out_ldt, int64_t out_ldh,
+             const int32_t *positions, const double *freqs, int rot, int layout, double mscale, int inverse, int64_t T, int H,
+             int D, void *stream) {
+    g_err[0] = '\0';
+    if (!mmq::type_ok(type) || !mmq::type_ok(out_type)) return refuse("unknown type %d", mmq::type_ok(type) ? out_type : type);
+    const char *bad = mmq::check_tokens(T, H);
+    if (!bad) bad = mmq::check_rope(D, rot, layout);
+    if (!bad) bad = mmq::check_strides(ldt, ldh);
+    if (!bad) bad = mmq::check_out_strides(T, H, D, out_ldt, out_ldh);
+    if (bad) return refuse("rope T=%lld H=%d D=%d: %s", (long long)T, H, D, bad);
+    if (T == 0) return 1;
+    if (!x || !out) return refuse("null pointer argument");
+    if ((bad = check_rotation(positions, freqs, D, rot, layout, mscale))) return refuse("rope: %s", bad);
+    if (!aligned(x, mmq::type_bytes(type)) || !aligned(out, mmq::type_bytes(out_type)))
+        return refuse("input and output pointers must be aligned to their type");
+    if (x == out && (type != out_type || (T > 1 && ldt != out_ldt) || (H > 1 && ldh != out_ldh)))
+        return refuse("rope: in place, type and strides of input and output must be the same");
+    const int cus = gfx950_cus();
+    if (!cus) return 0;
+    return launched("rope", mmq::launch_rope(type, x, ldt, ldh, out_type, out, out_ldt, out_ldh, positions, freqs, rot, layout,
+                                             mscale, inverse != 0, T, H, D, cus, static_cast<hipStream_t>(stream)));
+}
+
+int64_t mmq_kv_cache_bytes(int64_t n_pages, int page, int heads, int D) {
+    g_err[0] = '\0';
+    if (const char *bad = mmq::check_kv_cache(n_pages, page, heads, D)) {
+        refuse("cache of %lld pages of %d, %d heads of %d: %s", (long long)n_pages, page, heads, D, bad);
+        return -1;
+    }
+    return n_pages * heads * (page / 16) * mmq::kv_tile_bytes(D);
+}
+
+int mmq_kv_write(int type, const void *k, int64_t k_ldt, int64_t k_ldh, const void *v, int64_t v_ldt, int64_t v_ldh,
+                 const int32_t *positions, const double *freqs, int rot, int layout, double mscale, const int32_t *slots,
+                 int64_t T, void *cache, int64_t n_pages, int page, int heads, int D, void *stream) {
+    g_err[0] = '\0';
+    if (!mmq::type_ok(type)) return refuse("unknown type %d", type);
+    const char *bad = mmq::check_kv_cache(n_pages, page, heads, D);
+    if (!bad) bad = mmq::check_tokens(T, heads);
+    if (!bad) bad = mmq::check_strides(k_ldt, k_ldh);
+    if (!bad) bad = mmq::check_strides(v_ldt, v_ldh);
+    if (bad) return refuse("cache write T=%lld, %lld pages of %d, %d heads of %d: %s", (long long)T, (long long)n_pages, page,
+                           heads, D, bad);
+    if (T == 0) return 1;
+    if (!k || !v || !slots || !cache) return refuse("null pointer argument");
+    if (freqs && (bad = check_rotation(positions, freqs, D, rot, layout, mscale))) return refuse("cache write: %s", bad);
+    if (!aligned(k, mmq::type_bytes(type)) || !aligned(v, mmq::type_bytes(type)))
+        return refuse("keys and values must be aligned to their type");
+    if (!aligned(slots, 4)) return refuse("slots must be 4-byte aligned");
+    if (!aligned(cache, 16)) return refuse("the cache must be 16-byte aligned");
+    const int cus = gfx950_cus();
+    if (!cus) return 0;
+    return launched("cache write", mmq::launch_kv_write(type, k, k_ldt, k_ldh, v, v_ldt, v_ldh, positions, freqs,
+                                                        freqs ? rot : 0, layout, mscale, slots, T, cache, n_pages, page,
+                                                        heads, D, cus, static_cast<hipStream_t>(stream)));
+}
+
+int mmq_kv_read(int type, const void *cache, int64_t n_pages, int page, int heads, int D, const int32_t *slots, int64_t T,
+                void *k, int64_t k_ldt, int64_t k_ldh, void *v, int64_t v_ldt, int64_t v_ldh, void *stream) {
+    g_err[0] = '\0';
+    if (!mmq::type_ok(type)) return refuse("unknown type %d", type);
+    const char *bad = mmq::check_kv_cache(n_pages, page, heads, D);
+    if (!bad) bad = mmq::check_tokens(T, heads);
+    if (!bad) bad = mmq::check_out_strides(T, heads, D, k_ldt, k_ldh);
+    if (!bad) bad = mmq::check_out_strides(T, heads, D, v_ldt, v_ldh);
+    if (bad) return refuse("cache read T=%lld, %lld pages of %d, %d heads of %d: %s", (long long)T, (long long)n_pages, page,
+                           heads, D, bad);
+    if (T == 0) return 1;
+    if (!k || !v || !slots || !cache) return refuse("null pointer argument");
+    if (!aligned(k, mmq::type_bytes(type)) || !aligned(v, mmq::type_bytes(type)))
+        return refuse("keys and values must be aligned to their type");
+    if (!aligned(slots, 4)) return refuse("slots must be 4-byte aligned");
+    if (!aligned(cache, 16)) return refuse("the cache must be 16-byte aligned");
+    const int cus = gfx950_cus();
+    if (!cus) return 0;
+    return launched("cache read", mmq::launch_kv_read(type, cache, n_pages, page, heads, D, slots, T, k, k_ldt, k_ldh, v, v_ldt,
+                                                      v_ldh, cus, static_cast<hipStream_t>(stream)));
+}
+
+int64_t mmq_attention_workspace_bytes(int64_t T, int64_t n_seqs, int64_t max_q, int q_heads, int kv_heads, int D,
+                                      int64_t max_pages, int page) {
+    g_err[0] = '\0';
+    if (const char *bad = mmq::check_attention(T, n_seqs, q_heads, kv_heads, D, max_pages, page, max_q)) {
+        refuse("attention: %s", bad);
+        return -1;
+    }
+    if (T == 0 || n_seqs == 0) return 0;
+    const int cus = gfx950_cus();
+    if (!cus) return -1;
+    mmq::AttnPlan p;
+    char why[256];
+    if (!mmq::make_plan_attention(T, n_seqs, q_heads, kv_heads, D, max_pages, page, max_q, cus, &p, why, sizeof(why))) {
+        refuse("attention: %s", why);
+        return -1;
+    }
+    return p.few_bytes + p.tile_bytes;
+}
+
+int mmq_attention_i8(int type, const void *q, int64_t q_ldt, int64_t q_ldh, const void *cache, int64_t n_pages, int page,
+                     const int32_t *page_table, int64_t max_pages, const int32_t *lens, const int32_t *q_offsets,
+                     int64_t n_seqs, int64_t T, int64_t max_q, int q_heads, int kv_heads, int D, float scale, int64_t window,
+                     int out_type, void *out, int64_t out_ldt, int64_t out_ldh, void *workspace, int64_t workspace_bytes,
+                     void *stream) {
+    g_err[0] = '\0';
+    if (type != mmq::TYPE_BF16 && type != mmq::TYPE_F16) return refuse("attention: the queries must be bf16 or fp16");
+    if (out_type != type && out_type != mmq::TYPE_F32) return refuse("attention: the output must be fp32 or of the queries' type");
+    const char *bad = mmq::check_attention(T, n_seqs, q_heads, kv_heads, D, max_pages, page, max_q);
+    if (!bad) bad = mmq::check_kv_cache(n_pages, page, kv_heads, D);
+    if (!bad) bad = mmq::check_strides(q_ldt, q_ldh);
+    if (!bad) bad = mmq::check_out_strides(T, q_heads, D, out_ldt, out_ldh);
+    if (!bad && !(scale - scale == 0.0f)) bad = "the scale must be finite";
+    if (!bad && window < 0) bad = "the window must be at least 0 (0: none)";
+    if (bad) return refuse("attention T=%lld, %lld sequences, %d on %d heads of %d: %s", (long long)T, (long long)n_seqs, q_heads,
+                           kv_heads, D, bad);
+    if (T == 0 || n_seqs == 0) return 1;
+    if (!q || !cache || !lens || !q_offsets || !out || (!page_table && max_pages > 0)) return refuse("null pointer argument");
+    if (!aligned(q, 2) || !aligned(out, mmq::type_bytes(out_type))) return refuse("queries and output must be aligned to their type");
+    if (!aligned(cache, 16)) return refuse("the cache must be 16-byte aligned");
+    if (!aligned(page_table, 4) || !aligned(lens, 4) || !aligned(q_offsets, 4))
+        return refuse("page table, lengths and offsets must be 4-byte aligned");
+    const int cus = gfx950_cus();
+    if (!cus) return 0;
+    mmq::AttnPlan p;
+    char why[256];
+    if (!mmq::make_plan_attention(T, n_seqs, q_heads, kv_heads, D, max_pages, page, max_q, cus, &p, why, sizeof(why)))
+        return refuse("attention: %s", why);
+    const int64_t need = p.few_bytes + p.tile_bytes;
+    if (need > 0 && (!workspace || workspace_bytes < need))
+        return refuse("attention needs a workspace of %lld bytes, got %lld", (long long)need,
+                      (long long)(workspace ? workspace_bytes : 0));
+    if (need > 0 && !aligned(workspace, 16)) return refuse("the workspace must be 16-byte aligned");
+    // a window past the longest sequence is none
+    const int w = window >= (int64_t(1) << 30) ? 0 : int(window);
+    return launched("attention", mmq::launch_attention(p, type, q, q_ldt, q_ldh, cache, n_pages, page, page_table, max_pages,
+                                                       lens, q_offsets, n_seqs, T, max_q, q_heads, kv_heads, D, scale, w,
+                                                       out_type, out, out_ldt, out_ldh, workspace,
+                                                       static_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"

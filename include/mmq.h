@@ -406,6 +406,133 @@ int mmq_grouped_gemm_i8(int type, const void *xq, int64_t ldx, const float *xs, 
  * the kernel, its tile and grid into buf.  Returns as mmq_plan_for_limits. */
 int mmq_plan_i8(int64_t M, int64_t N, int64_t K, int n_experts, int cu_count, char *buf, int64_t len);
 
+/* ---------------------------------------------------------------------------
+ * Between a layer's q/k/v product and its output product: rotary positions,
+ * a paged cache of keys and values in per-token int8, and attention of new
+ * tokens over it.
+ *
+ * Operands [T, H, D] (tokens, heads, values of a head) have adjacent values and
+ * strides in ELEMENTS between tokens (ldt) and between heads (ldh), so that
+ * q, k and v may be slices of one product's output, or [H, T, D] in memory;
+ * pointers are aligned to their type.  Strides of an operand that is only
+ * read are 0..2^40; of one that is written, no two elements may share a place.
+ * T <= 2^24, H <= 1024.  T = 0 returns 1 and launches nothing.
+ * These entry points keep no state: calls may overlap in time on any streams
+ * (each with its own workspace, and none writing a cache slot that another
+ * reads or writes), and be captured into graphs and replayed; positions,
+ * slots, tables, lengths and offsets are read from the device at every replay.
+ * The other conventions are those at the top of this file, except that inputs
+ * need not be finite: what infinities and NaN give is said at each.
+ * ------------------------------------------------------------------------- */
+#define MMQ_ROPE_HALF 0            /* pair i of a head: values i and i + rot/2 */
+#define MMQ_ROPE_INTERLEAVED 1     /* pair i: values 2i and 2i + 1 */
+
+#define MMQ_ROPE_PLAIN 0
+#define MMQ_ROPE_LINEAR 1
+#define MMQ_ROPE_BANDS 2
+#define MMQ_ROPE_YARN 3
+
+/* Rotary frequencies (host only, no device needed): freqs[i], i < rot/2, in
+ * radians per position, HOST memory; *mscale, the factor on rotated values.
+ *   f = base^(-2i/rot), turns = f * original / (2 pi)
+ *   PLAIN   f
+ *   LINEAR  f / factor
+ *   BANDS   f/factor * (1-k) + f * k, k = (turns - low) / (high - low) in 0..1
+ *   YARN    the same with k = 1 - (i - a) / max(b - a, 0.001) in 0..1, where
+ *           a = max(floor(pair(high)), 0), b = min(ceil(pair(low)), rot - 1),
+ *           pair(n) = rot ln(original / (2 pi n)) / (2 ln base);
+ *           mscale = 0.1 ln(factor) + 1 for factor > 1 (else, and for the
+ *           other scalings, 1).
+ * rot: even, 2..512; base > 1; factor > 0 (not read by PLAIN); 0 < low < high
+ * and original >= 1 (read by BANDS and YARN only). */
+int mmq_rope_frequencies(int scaling, int rot, double base, double factor, double low, double high, int64_t original,
+                         double *freqs, double *mscale);
+
+/* Turn the first `rot` values of every head by its token's position; the rest
+ * is copied (rounded to out_type).  For a pair (a, b) and the angle
+ * phi = positions[t] * freqs[i]:
+ *   a' = mscale * (a cos phi - b sin phi),  b' = mscale * (b cos phi + a sin phi)
+ * with the angle, cosine, sine, products and sum in 64 bits, rounded to fp32
+ * and then to out_type.  inverse != 0 turns by -phi: with the same mscale, the
+ * gradient of the rotation with respect to x, given that of its output.
+ *   x: [T, H, D] of `type`; out: [T, H, D] of out_type, may be x itself (same
+ *   type and strides), else must not overlap it; positions: int32 [T]; freqs:
+ *   fp64 [rot/2] (device).  D: a multiple of 8 in 8..512; rot: even, 2..D. */
+int mmq_rope(int type, const void *x, int64_t ldt, int64_t ldh, int out_type, void *out, int64_t out_ldt, int64_t out_ldh,
+             const int32_t *positions, const double *freqs, int rot, int layout, double mscale, int inverse, int64_t T, int H,
+             int D, void *stream);
+
+/* The paged cache: n_pages pages of `page` tokens (16, 32, 64, 128 or 256) for
+ * `heads` key/value heads of D = 64, 128 or 256 values, each row (a key or a
+ * value vector of one token and head) as int8 codes and one fp32 scale by the
+ * rule of mmq_quantize_i8.  Slot s is place s % page of page s / page.
+ * The layout is this library's own (mmq_kv_write and mmq_kv_read convert):
+ * [page][head][page/16] tiles of 32 D + 128 bytes, each K codes
+ * [D/16][16 tokens][16], V codes [D/64][4][64 values][4 tokens], K scales
+ * [16], V scales [16].  Slots never written hold nothing in particular and
+ * need no preparation.
+ * mmq_kv_cache_bytes: n_pages * heads * page * (2 D + 8), or -1 (reason in
+ * mmq_last_error).  The cache is device memory, 16-byte aligned, the caller's. */
+int64_t mmq_kv_cache_bytes(int64_t n_pages, int page, int heads, int D);
+
+/* Quantize T tokens' keys and values and write them to their slots.
+ *   k, v: [T, heads, D] of `type`; slots: int32 [T].  A token whose slot is
+ *   outside 0..n_pages*page-1 (-1, say) is passed over.  Slots of a call must
+ *   differ: one that two tokens name holds unspecified codes and scales
+ *   afterwards (no other slot is affected).  Every other byte of the cache is
+ *   left as it was.
+ *   freqs NULL: k is stored as it is (positions, rot, layout and mscale are
+ *   not read).  Else k is turned as by mmq_rope first, rounded to fp32 only.
+ * A row that holds an infinity or NaN gets codes 0 and scale NaN. */
+int mmq_kv_write(int type, const void *k, int64_t k_ldt, int64_t k_ldh, const void *v, int64_t v_ldt, int64_t v_ldh,
+                 const int32_t *positions, const double *freqs, int rot, int layout, double mscale, const int32_t *slots,
+                 int64_t T, void *cache, int64_t n_pages, int page, int heads, int D, void *stream);
+
+/* The values that slots hold: code times scale in fp32, rounded to `type`.
+ *   k, v: [T, heads, D] of `type`; slots: int32 [T], in any order, repeats
+ *   allowed.  Rows of a slot outside the cache are left as they were. */
+int mmq_kv_read(int type, const void *cache, int64_t n_pages, int page, int heads, int D, const int32_t *slots, int64_t T,
+                void *k, int64_t k_ldt, int64_t k_ldh, void *v, int64_t v_ldt, int64_t v_ldh, void *stream);
+
+/* Attention of new tokens over the cache that already holds them.
+ * Sequence b has lens[b] tokens in the cache, token t at place t % page of
+ * page page_table[b][t / page]; the last q_offsets[b+1] - q_offsets[b] of them
+ * are its new ones, rows q_offsets[b].. of q.  The new token at position p of
+ * its sequence sees keys 0..p, or with a window w > 0 the last w of them,
+ * p-w+1..p.  For each of its query heads h, with k_t and v_t the values that
+ * the cache holds for head h / (q_heads / kv_heads),
+ *   out = sum_t softmax_t(scale * q . k_t) v_t.
+ *   q: [T, q_heads, D], bf16 or fp16; out: the same shape, of q's type or fp32;
+ *   page_table: int32 [n_seqs][max_pages]; lens: int32 [n_seqs]; q_offsets:
+ *   int32 [n_seqs + 1], not decreasing.
+ *   max_q: the most new tokens of a sequence; a sequence with more has only
+ *   its first max_q computed.
+ * Rounding: q and the codes enter the products as they are, sums are fp32;
+ * exp(..) times a value's scale is rounded to q's type for the second
+ * product, and the output once to its own.
+ * A row that sees no key (lens 0, or fewer tokens than new ones) gets zeros.
+ * Keys on a page whose number is outside 0..n_pages-1 are not seen.  A seen
+ * key or value with scale NaN makes its rows NaN; what is not seen has no
+ * effect, whatever it holds.  Rows of out outside every sequence, and past
+ * max_q, are left as they were.  Lengths are clamped to 0..max_pages*page and
+ * offsets to 0..T; where offsets decrease, rows between them are unspecified,
+ * but nothing outside the buffers is read or written.
+ * T * q_heads <= 2^30; n_seqs <= 2^20; max_pages * page <= 2^30.
+ * The same bits on every run; which shares a sequence's keys are split into
+ * (and so the last bits) depends on the whole batch's lengths.
+ * workspace: mmq_attention_workspace_bytes for the same sizes (0: may be NULL),
+ * 16-byte aligned, the caller's; its contents need no preparation.  Calls
+ * that overlap in time must not share one.
+ * mmq_attention_workspace_bytes returns -1 for sizes that are refused; the
+ * size depends on the current device (its compute units). */
+int64_t mmq_attention_workspace_bytes(int64_t T, int64_t n_seqs, int64_t max_q, int q_heads, int kv_heads, int D,
+                                      int64_t max_pages, int page);
+int mmq_attention_i8(int type, const void *q, int64_t q_ldt, int64_t q_ldh, const void *cache, int64_t n_pages, int page,
+                     const int32_t *page_table, int64_t max_pages, const int32_t *lens, const int32_t *q_offsets,
+                     int64_t n_seqs, int64_t T, int64_t max_q, int q_heads, int kv_heads, int D, float scale, int64_t window,
+                     int out_type, void *out, int64_t out_ldt, int64_t out_ldh, void *workspace, int64_t workspace_bytes,
+                     void *stream);
+
 /* Test entry: the exact int32 block dots I[m,n,b] through the same staging
  * and matrix-core code as the tiled GEMM of format `fmt` (MMQ_FMT_Q8_0,
  * MMQ_FMT_Q4_K or MMQ_FMT_Q5_K; always the tile kernel, whatever M),
