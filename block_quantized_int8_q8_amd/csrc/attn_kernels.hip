@@ -54,6 +54,7 @@ struct AttnArgs {
     float *part;              // shares: outputs, then (reference, sum) pairs
     int split, target;        // most shares; workgroups that fill the device
     int units;                // rows kernel: B; tile kernel: row tiles there can be
+    int few_rows;             // most rows of a sequence of the rows kernel
 };
 
 // --- 16-bit types -----------------------------------------------------------
@@ -122,7 +123,7 @@ __device__ __forceinline__ Seq sequence(const AttnArgs &a, int b) {
     const int len = clamp_len(a, a.lens[b]);
     return Seq{s, min(n, a.max_q), len, len - n};
 }
-__device__ __forceinline__ bool has_few_rows(const AttnArgs &a, int n) { return int64_t(n) * a.G <= kAttnFewRows; }
+__device__ __forceinline__ bool has_few_rows(const AttnArgs &a, int n) { return int64_t(n) * a.G <= a.few_rows; }
 
 // The keys [begin, end) that tokens first .. last of a sequence see among
 // them; begin is rounded down to a tile of 16.
@@ -183,6 +184,7 @@ __device__ __forceinline__ int few_chunk(const AttnArgs &a) {
 // ---------------------------------------------------------------------------
 constexpr float kSlack = 8.0f;
 constexpr float kNarrowTop = 6.0f, kNarrowSum = 60.0f;
+constexpr float kTop = 6.0f;
 
 // --- rows kernel ------------------------------------------------------------
 template <typename T, typename O, int D, int RT>
@@ -421,12 +423,11 @@ __global__ __launch_bounds__(64 * WAVES) void k_attn_tile(AttnArgs a) {
     typedef typename Half<T>::x8 x8;
     constexpr int THREADS = 64 * WAVES, BM = 32 * WAVES, TILE = int(kv_tile_bytes(D));
     constexpr int KS = D / 16, DT = D / 32;              // steps of the first product, column tiles of the second
-    constexpr int LOADS = 8 * D / THREADS;               // 16-byte loads of a lane for 64 keys and values
-    constexpr int BUF = 2 * 64 * D * 2;                  // K then V, 16 bits each
+    constexpr int LOADS = 8 * D / THREADS;               // 16-byte loads of a lane for 64 keys and 64 values
     constexpr float NEG = -__builtin_inff();
-    static_assert(8 * D % THREADS == 0, "whole loads");
-    __shared__ __align__(16) uint8_t S[2][BUF];
-    __shared__ __align__(16) float S_ks[2][64], S_vs[2][64], S_lv[2][64];
+    static_assert(8 * D % (2 * THREADS) == 0, "whole loads of keys and of values");
+    __shared__ __align__(16) uint8_t S_k[2][128 * D], S_v[2][128 * D];
+    __shared__ __align__(16) float S_ks[4][64], S_lv[4][64], S_rv[4][64];
     const int tid = threadIdx.x, lane = tid & 63, wv = __builtin_amdgcn_readfirstlane(tid >> 6), col = lane & 31, hf = lane >> 5;
     const int h = blockIdx.x % a.Hkv, rest = blockIdx.x / a.Hkv, share = rest / a.units;
     int b, in, of;
@@ -440,6 +441,7 @@ __global__ __launch_bounds__(64 * WAVES) void k_attn_tile(AttnArgs a) {
     const int begin = all.begin + min(int64_t(share) * chunk, int64_t(all.end - all.begin)), end = min(int64_t(all.end), int64_t(begin) + chunk);
     const bool alone = all.end - all.begin <= chunk;
     if (begin >= end && share > 0) return;
+    const int steps = (end - begin + 63) / 64;
 
     // this lane's row
     const int r = row0 + 32 * wv + col, tok = r / a.G;
@@ -451,12 +453,12 @@ __global__ __launch_bounds__(64 * WAVES) void k_attn_tile(AttnArgs a) {
 #pragma unroll
         for (int k = 0; k < KS; k++) q[k] = load_x8(qr + 16 * k + 8 * hf);
     }
-    // what the wave's rows see: all of keys (lo_all, hi_all], something of (lo_any, hi_any]
+    // the wave's rows see all of keys (lo_all, hi_all], and something in steps [from, to]
     const int wr0 = row0 + 32 * wv, wr1 = min(wr0 + 32, rows) - 1;
-    const bool active = wr0 < rows;
-    const int p_lo = s.pos0 + wr0 / a.G, p_hi = s.pos0 + wr1 / a.G;
-    const int hi_any = p_hi, hi_all = p_lo;
-    const int lo_any = a.window ? p_lo - a.window : -1, lo_all = a.window ? p_hi - a.window : -1;
+    const int hi_all = s.pos0 + wr0 / a.G, hi_any = s.pos0 + wr1 / a.G;
+    const int lo_all = a.window ? hi_any - a.window : -1, lo_any = a.window ? hi_all - a.window : -1;
+    const bool active = wr0 < rows && hi_any >= begin && lo_any < end;
+    const int from = active ? max(lo_any + 1 - begin, 0) / 64 : steps, to = active ? min((hi_any - begin) / 64, steps - 1) : -1;
 
     float m = NEG, l = 0.0f;
     f32x16 o[DT];
@@ -465,145 +467,211 @@ __global__ __launch_bounds__(64 * WAVES) void k_attn_tile(AttnArgs a) {
 #pragma unroll
         for (int i = 0; i < 16; i++) o[d][i] = 0.0f;
 
-    const int steps = (end - begin + 63) / 64;
+    // Load i of a wave: 64 chunks of 16 bytes of the keys (of step `step`) or,
+    // behind those, of the values (of the step before).
     u32x4 st[LOADS];
     float st_scale = 0.0f;
-    int tiles = -1;                                       // of 16 steps: lane 4 i + j holds 16-key tile j of step i
-    auto look_up = [&](int step) {
-        const int k16 = begin / 16 + 4 * step + lane;
-        tiles = 16 * k16 < end ? cache_tile(a, b, h, k16) : -1;
-    };
-    int valid[2];                                         // of the two buffers: which of their four tiles are there
-    auto load = [&](int step) {
-        if ((step & 15) == 0) look_up(step);
+    int tk = -1, tv = -1;                                 // cache tiles of 16 steps: lane 4 i + j holds 16-key tile j of step i
+    int valid = 0;                                        // four bits a step, of four steps: which of its tiles are there
+    auto load = [&](int step) __attribute__((always_inline)) {
+        tv = tk;
+        if ((step & 15) == 0) {
+            const int k16 = begin / 16 + 4 * step + lane;
+            tk = 16 * k16 < end ? cache_tile(a, b, h, k16) : -1;
+        }
+        const unsigned long long ok = __ballot(tk >= 0);
+        valid = (valid & ~(15 << 4 * (step & 3))) | (int(ok >> (4 * (step & 15))) & 15) << 4 * (step & 3);
 #pragma unroll
         for (int i = 0; i < LOADS; i++) {
-            const int c = i * THREADS + wv * 64, part = c / D, at = c % D;      // parts: K and V of each 16-key tile
-            const int t = max(__builtin_amdgcn_readlane(tiles, 4 * (step & 15) + part / 2), 0);
-            st[i] = *reinterpret_cast<const u32x4 *>(a.cache + int64_t(t) * TILE + (part & 1) * 16 * D + (at + lane) * 16);
+            const int c = i * THREADS + wv * 64;
+            const bool is_v = i >= LOADS / 2;
+            const int part = c / D & 3, at = c % D;
+            const int t = max(is_v ? __builtin_amdgcn_readlane(tv, 4 * ((step - 1) & 15) + part)
+                                   : __builtin_amdgcn_readlane(tk, 4 * (step & 15) + part), 0);
+            st[i] = *reinterpret_cast<const u32x4 *>(a.cache + int64_t(t) * TILE + (is_v ? 16 * D : 0) + (at + lane) * 16);
         }
-        if (tid < 128) {                                  // wave 0: key scales; wave 1: value scales
-            const int t = __shfl(tiles, 4 * (step & 15) + (lane >> 4));
+        if (wv < 2) {                                     // wave 0: key scales; wave 1: value scales
+            const int t = __shfl(tk, 4 * (step & 15) + (lane >> 4));
             st_scale = t >= 0 && begin + 64 * step + lane < end
                            ? reinterpret_cast<const float *>(a.cache + int64_t(t) * TILE + 32 * D)[16 * wv + (lane & 15)]
                            : 0.0f;
         }
     };
-    auto store = [&](int step) {
-        const int buf = step & 1;
-        const unsigned long long ok = __ballot(tiles >= 0);
-        valid[buf] = int(ok >> (4 * (step & 15))) & 15;
-#pragma unroll
-        for (int i = 0; i < LOADS; i++) {
-            const int c = i * THREADS + wv * 64, part = c / D, at = c % D, t16 = part / 2;
-            uint32_t w[4][2];
-#pragma unroll
-            for (int k = 0; k < 4; k++) Half<T>::codes(st[i][k], w[k]);
-            if (!(part & 1)) {
-                // K: lane = (chunk of 16 d, token): fragment (32 keys, 16 d): [half of d][key][8 d]
-                const int ch = (at + lane) >> 4, key = 16 * (t16 & 1) + (lane & 15);
-                uint8_t *p = S[buf] + ((t16 >> 1) * KS + ch) * 1024 + key * 16;
-                *reinterpret_cast<u32x4 *>(p) = u32x4{w[0][0], w[0][1], w[1][0], w[1][1]};
-                *reinterpret_cast<u32x4 *>(p + 512) = u32x4{w[2][0], w[2][1], w[3][0], w[3][1]};
-            } else {
-                // V: lane = (four tokens g, four d): fragment (16 keys, 32 d): [g & 1][d][g >> 1][4 tokens]
-                const int v64 = at / 64, gg = lane >> 4;
-                uint8_t *p = S[buf] + 128 * D + (t16 * DT + 2 * v64) * 1024 + (gg & 1) * 512 + (lane & 15) * 16 + (gg >> 1) * 8;
-#pragma unroll
-                for (int k = 0; k < 4; k++) *reinterpret_cast<uint2 *>(p + (k >> 1) * 1024 + (k & 1) * 256) = make_uint2(w[k][0], w[k][1]);
-            }
-        }
-        if (wv == 0) S_ks[buf][lane] = st_scale * a.scale;
-        if (wv == 1) {
-            S_vs[buf][lane] = st_scale;
-            if (Half<T>::NARROW) S_lv[buf][lane] = __builtin_amdgcn_logf(st_scale);
+    // Unit u of the conversion to 16 bits: dword u % 4 of load u / 4.
+    uint32_t cw[2][2];
+    auto store = [&](int step, int u) __attribute__((always_inline)) {
+        const int i = u / 4, k = u % 4, c = i * THREADS + wv * 64, part = c / D & 3, at = c % D;
+        Half<T>::codes(st[i][k], cw[k & 1]);
+        if (i < LOADS / 2) {
+            // K: lane = (chunk of 16 d, token): fragment (32 keys, 16 d): [half of d][key][8 d]
+            const int ch = (at + lane) >> 4, key = 16 * (part & 1) + (lane & 15);
+            uint8_t *p = S_k[step & 1] + ((part >> 1) * KS + ch) * 1024 + key * 16;
+            if (k & 1) *reinterpret_cast<u32x4 *>(p + (k >> 1) * 512) = u32x4{cw[0][0], cw[0][1], cw[1][0], cw[1][1]};
+        } else {
+            // V: lane = (four tokens g, four d): fragment (16 keys, 32 d): [g & 1][d][g >> 1][4 tokens]
+            const int gg = lane >> 4;
+            uint8_t *p = S_v[(step - 1) & 1] + (part * DT + at / 32) * 1024 + (gg & 1) * 512 + (lane & 15) * 16 + (gg >> 1) * 8;
+            *reinterpret_cast<uint2 *>(p + (k >> 1) * 1024 + (k & 1) * 256) = make_uint2(cw[k & 1][0], cw[k & 1][1]);
         }
     };
-    if (steps > 0) {
-        load(0);
-        store(0);
-        if (steps > 1) load(1);
-    }
-    for (int step = 0; step < steps; step++) {
-        const int buf = step & 1, key0 = begin + 64 * step;
-        __syncthreads();
-        if (step + 1 < steps) {
-            store(step + 1);
-            if (step + 2 < steps) load(step + 2);
+    auto store_scales = [&](int step) __attribute__((always_inline)) {
+        if (wv == 0) S_ks[step & 3][lane] = st_scale * a.scale;
+        if (wv == 1) {
+            // A row of zeros has scale 0: any other does for its codes, and
+            // the step's smallest keeps its logarithm among the others.
+            const bool none = st_scale < 0x1p-126f;
+            float least = none ? __builtin_inff() : st_scale;
+#pragma unroll
+            for (int x = 32; x; x >>= 1) least = fminf(least, __shfl_xor(least, x));
+            const float sc = !none ? st_scale : least < __builtin_inff() ? least : 0x1p-20f;
+            S_lv[step & 3][lane] = __builtin_amdgcn_logf(sc);
+            S_rv[step & 3][lane] = sc == sc ? 1.0f / sc : 1.0f;       // NaN reaches a row by the logarithm, if it is seen
         }
-        if (!active || key0 > hi_any || key0 + 63 <= lo_any) continue;
-        const uint8_t *K = S[buf], *V = K + 128 * D;
-        f32x16 sc[2];
+    };
+    auto store_all = [&](int step) __attribute__((always_inline)) {
+#pragma unroll
+        for (int u = 0; u < 4 * LOADS; u++) store(step, u);
+        store_scales(step);
+    };
+    // Element e of a lane's 32 scores of a step: key 8 (e / 4) + 4 hf + e % 4.
+    auto scaled = [&](float x, float k, float v) __attribute__((always_inline)) { return __builtin_fmaf(x, k, v); };
+    auto four = [&](const float (*S)[64], int step, int chunk) __attribute__((always_inline)) {
+        return *reinterpret_cast<const f32x4 *>(S[step & 3] + 4 * hf + 8 * chunk);
+    };
+    // The scores of one step, alone: where a wave's rows begin to see keys.
+    auto first_scores = [&](int step, f32x16 (&sc)[2], float &top) __attribute__((always_inline)) {
+        const uint8_t *K = S_k[step & 1] + lane * 16;
 #pragma unroll
         for (int j = 0; j < 2; j++) {
 #pragma unroll
             for (int i = 0; i < 16; i++) sc[j][i] = 0.0f;
 #pragma unroll
-            for (int k = 0; k < KS; k++)
-                sc[j] = Half<T>::mfma32(*reinterpret_cast<const x8 *>(K + (j * KS + k) * 1024 + lane * 16), q[k], sc[j]);
+            for (int k = 0; k < KS; k++) sc[j] = Half<T>::mfma32(*reinterpret_cast<const x8 *>(K + (j * KS + k) * 1024), q[k], sc[j]);
         }
-        const bool whole = valid[buf] == 15 && key0 + 63 <= hi_all && key0 > lo_all;
-        // register i of half j: key 32 j + 8 (i / 4) + 4 hf + i % 4
-        float top = NEG, low = NEG;
+        top = NEG;
 #pragma unroll
-        for (int j = 0; j < 2; j++)
+        for (int ch = 0; ch < 8; ch++) {
+            const f32x4 k4 = four(S_ks, step, ch), v4 = four(S_lv, step, ch);
 #pragma unroll
-            for (int x = 0; x < 4; x++) {
-                const int at = 32 * j + 8 * x + 4 * hf;
-                const f32x4 ks = *reinterpret_cast<const f32x4 *>(&S_ks[buf][at]);
+            for (int y = 0; y < 4; y++) {
+                sc[ch / 4][4 * (ch % 4) + y] = scaled(sc[ch / 4][4 * (ch % 4) + y], k4[y], v4[y]);
+                top = fmaxf(top, sc[ch / 4][4 * (ch % 4) + y]);
+            }
+        }
+    };
+    // One step.  `sc` holds its scaled scores and `top` their largest, and
+    // takes the next step's.  Two runs of D / 8 products each, with the VALU
+    // work of a step spread between them:
+    //   the next step's scores     this step's exponentials
+    //   this step's output         the next scores' scales and maximum, and
+    //                              the conversion of the step after that
+    // The order is written out and pinned, with fragments four products ahead.
+    float top = NEG;
+    auto body = [&](int step, f32x16 (&sc)[2]) __attribute__((always_inline)) {
+        constexpr int N = D / 8, E = 32 / N, AHEAD = 4;
+        const int key0 = begin + 64 * step;
+        __syncthreads();
+        {
+            const uint8_t *K = S_k[(step + 1) & 1] + lane * 16, *V = S_v[step & 1] + lane * 16;
+            x8 fr[AHEAD];
 #pragma unroll
-                for (int y = 0; y < 4; y++) sc[j][4 * x + y] *= ks[y];
-                if (!whole) {
+            for (int g = 0; g < AHEAD; g++) fr[g] = *reinterpret_cast<const x8 *>(K + g * 1024);
+            f32x4 r4 = four(S_rv, step, 0);
+            const int there4 = valid >> 4 * (step & 3) & 15;
+            if (!(there4 == 15 && key0 + 63 <= hi_all && key0 > lo_all)) {
+                top = NEG;
 #pragma unroll
-                    for (int y = 0; y < 4; y++) {
-                        const int key = key0 + at + y;
-                        const bool seen = (valid[buf] >> (2 * j + x / 2) & 1) && key <= pos && key > first;
-                        if (!seen) sc[j][4 * x + y] = NEG;
-                    }
-                }
-                f32x4 lv = {0, 0, 0, 0};
-                if (Half<T>::NARROW) lv = *reinterpret_cast<const f32x4 *>(&S_lv[buf][at]);
-#pragma unroll
-                for (int y = 0; y < 4; y++) {
-                    top = fmaxf(top, sc[j][4 * x + y]);
-                    if (Half<T>::NARROW) {
-                        // a masked score is -inf and its sum with a scale that is 0, infinite or NaN must not count
-                        const float u = sc[j][4 * x + y] + lv[y];
-                        low = fmaxf(low, sc[j][4 * x + y] == NEG ? NEG : u);
-                    }
+                for (int e = 0; e < 32; e++) {
+                    const int key = key0 + 8 * (e / 4) + 4 * hf + e % 4;
+                    if (!((there4 >> (e / 8) & 1) && key <= pos && key > first)) sc[e / 16][e % 16] = NEG;
+                    top = fmaxf(top, sc[e / 16][e % 16]);
                 }
             }
-        float want = Half<T>::NARROW ? fmaxf(low - kNarrowTop, top - kNarrowSum) : top;
-        want = fmaxf(want, __shfl_xor(want, 32));
-        if (__any(want > m + kSlack || (m == NEG && want > NEG))) {
-            const float to = fmaxf(m, want), f = to == NEG ? 1.0f : __builtin_amdgcn_exp2f(m - to);
-            m = to;
-            l *= f;
+            float want = top - kTop;
+            want = fmaxf(want, __shfl_xor(want, 32));
+            if (__any(want > m + kSlack || (m == NEG && want > NEG))) {
+                const float up = fmaxf(m, want), f = up == NEG ? 1.0f : __builtin_amdgcn_exp2f(m - up);
+                m = up;
+                l *= f;
 #pragma unroll
-            for (int d = 0; d < DT; d++)
+                for (int d = 0; d < DT; d++)
 #pragma unroll
-                for (int i = 0; i < 16; i++) o[d][i] *= f;
-        }
-        const float ref = m == NEG ? 0.0f : m;
-#pragma unroll
-        for (int c = 0; c < 4; c++) {                     // 16 keys: registers 8 (c % 2) .. + 7 of half c / 2
-            T w[8];
-#pragma unroll
-            for (int x = 0; x < 2; x++) {
-                const f32x4 vs = *reinterpret_cast<const f32x4 *>(&S_vs[buf][16 * c + 8 * x + 4 * hf]);
-#pragma unroll
-                for (int y = 0; y < 4; y++) {
-                    const float t = sc[c / 2][8 * (c % 2) + 4 * x + y], p = __builtin_amdgcn_exp2f(t - ref);
-                    l += p;
-                    w[4 * x + y] = T(!whole && t == NEG ? 0.0f : p * vs[y]);
-                }
+                    for (int i = 0; i < 16; i++) o[d][i] *= f;
             }
-            x8 p8;
-            __builtin_memcpy(&p8, w, 16);
+            const float ref = m == NEG ? 0.0f : m;
+            union { T w[32]; x8 p[4]; } u;
+            float pair = 0.0f;
+            f32x16 nx[2];
 #pragma unroll
-            for (int d = 0; d < DT; d++)
-                o[d] = Half<T>::mfma32(*reinterpret_cast<const x8 *>(V + (c * DT + d) * 1024 + lane * 16), p8, o[d]);
+            for (int j = 0; j < 2; j++)
+#pragma unroll
+                for (int i = 0; i < 16; i++) nx[j][i] = 0.0f;
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int g = 0; g < N; g++) {
+                nx[g / KS] = Half<T>::mfma32(fr[g % AHEAD], q[g % KS], nx[g / KS]);
+                fr[g % AHEAD] = *reinterpret_cast<const x8 *>(g + AHEAD < N ? K + (g + AHEAD) * 1024 : V + (g + AHEAD - N) * 1024);
+#pragma unroll
+                for (int e = g * E; e < g * E + E; e++) {
+                    const float p = __builtin_amdgcn_exp2f(sc[e / 16][e % 16] - ref);
+                    l = __builtin_fmaf(p, r4[e % 4], l);
+                    if (e % 4 == 3 && e < 31) r4 = four(S_rv, step, e / 4 + 1);
+                    if (e & 1) {
+                        u.w[e - 1] = T(pair);
+                        u.w[e] = T(p);
+                    }
+                    pair = p;
+                }
+                asm volatile("" : "+v"(l));               // summed here: put off, the sums would keep every p in a register
+                __builtin_amdgcn_sched_barrier(0);
+            }
+            f32x4 k4 = four(S_ks, step + 1, 0), v4 = four(S_lv, step + 1, 0);
+            top = NEG;
+#pragma unroll
+            for (int g = 0; g < N; g++) {
+                o[g % DT] = Half<T>::mfma32(fr[g % AHEAD], u.p[g / DT], o[g % DT]);
+                if (g + AHEAD < N) fr[g % AHEAD] = *reinterpret_cast<const x8 *>(V + (g + AHEAD) * 1024);
+#pragma unroll
+                for (int e = g * E; e < g * E + E; e++) {
+                    sc[e / 16][e % 16] = scaled(nx[e / 16][e % 16], k4[e % 4], v4[e % 4]);
+                    top = fmaxf(top, sc[e / 16][e % 16]);
+                    if (e % 4 == 3 && e < 31) {
+                        k4 = four(S_ks, step + 1, e / 4 + 1);
+                        v4 = four(S_lv, step + 1, e / 4 + 1);
+                    }
+                }
+                asm volatile("" : "+v"(top));
+                if ((g + 1) * 4 * LOADS % N == 0) store(step + 2, (g + 1) * 4 * LOADS / N - 1);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+            store_scales(step + 2);
         }
+        load(step + 3);
+    };
+    auto bring = [&](int step) __attribute__((always_inline)) {
+        __syncthreads();
+        store_all(step + 2);
+        load(step + 3);
+    };
+    // Buffers: load(s) and store(s) bring the keys of step s and the values of
+    // step s - 1 (past the last step: of tile 0, not used).  In step s the
+    // keys of s + 1 and the values of s are read; those of s + 2 and s + 1
+    // take the places of what step s - 1 has read.
+    if (steps > 0) {
+        f32x16 sc[2];
+        load(0);
+        store_all(0);
+        load(1);
+        store_all(1);
+        load(2);
+        __syncthreads();
+        int step = 0;
+        for (; step < min(from, steps); step++) bring(step);
+        if (from <= to) {
+            first_scores(from, sc, top);
+            for (; step <= to; step++) body(step, sc);
+        }
+        for (; step < steps; step++) bring(step);
     }
     l += __shfl_xor(l, 32);
     if (!there) return;
@@ -632,14 +700,16 @@ __global__ __launch_bounds__(64 * WAVES) void k_attn_tile(AttnArgs a) {
 }
 
 // ---------------------------------------------------------------------------
-// Joins shares: D / 4 lanes a row, the rows of one (sequence, head) or (tile,
-// head) a workgroup.  Rows whose keys were not split have been written.
+// Joins shares: D / 4 lanes a row; the others of a workgroup's lanes take
+// other shares of it (rows kernel: up to hundreds of shares, few rows) or
+// other rows (tile kernel: a few shares, many rows).  Rows whose keys were
+// not split have been written.
 // ---------------------------------------------------------------------------
 template <typename O, int D, int BM, bool TILES>
 __global__ __launch_bounds__(256) void k_attn_join(AttnArgs a) {
-    constexpr int LANES = D / 4, ROWS = 256 / LANES, GROUPS = (BM + ROWS - 1) / ROWS;
+    constexpr int LANES = D / 4, GROUPS = 256 / LANES, ROWS = TILES ? GROUPS : 1, BLOCKS = BM / ROWS;
     constexpr float NEG = -__builtin_inff();
-    const int group = blockIdx.x % GROUPS, unit = blockIdx.x / GROUPS, h = unit % a.Hkv;
+    const int block = blockIdx.x % BLOCKS, unit = blockIdx.x / BLOCKS, h = unit % a.Hkv;
     int b = unit / a.Hkv, in = 0, of = 1;
     if (TILES) {
         if (!find_tile<BM>(a, unit / a.Hkv, b, in, of)) return;
@@ -647,26 +717,48 @@ __global__ __launch_bounds__(256) void k_attn_join(AttnArgs a) {
         in = of - 1 - __builtin_amdgcn_readfirstlane(in);
     }
     const Seq s = sequence(a, b);
-    if (s.n == 0 || has_few_rows(a, s.n) == TILES) return;
-    const int rows = s.n * a.G, row0 = in * BM;
+    const int rows = s.n * a.G, row0 = in * BM, group = threadIdx.x / LANES;
+    if (s.n == 0 || has_few_rows(a, s.n) == TILES || row0 + block * ROWS >= rows) return;
     const Range all(a, s, row0 / a.G, (min(row0 + BM, rows) - 1) / a.G);
     const int chunk = TILES ? tile_chunk(a, all) : few_chunk(a);
     const int shares = (all.end - all.begin + chunk - 1) / chunk;
-    const int r = group * ROWS + threadIdx.x / LANES, d = 4 * (threadIdx.x % LANES);
-    if (shares <= 1 || r >= BM || row0 + r >= rows) return;
+    const int r = TILES ? block * ROWS + group : block, d = 4 * (threadIdx.x % LANES);
+    if (shares <= 1) return;
+    const bool there = row0 + r < rows;
     const int64_t slot0 = int64_t(unit) * a.split * BM + r;
     const float *ml = a.part + int64_t(a.units) * a.Hkv * a.split * BM * D;
-    float to = NEG;
-    for (int k = 0; k < shares; k++) to = fmaxf(to, ml[2 * (slot0 + int64_t(k) * BM)]);
+    float to = NEG, sum = 0.0f;
     f32x4 v = {0, 0, 0, 0};
-    float sum = 0.0f;
-    for (int k = 0; k < shares; k++) {
-        const int64_t slot = slot0 + int64_t(k) * BM;
-        const float m = ml[2 * slot], f = m == NEG ? 0.0f : __builtin_amdgcn_exp2f(m - to);
-        // a share that saw no finite maximum adds nothing, unless it holds a NaN
-        sum += m == NEG ? ml[2 * slot + 1] : ml[2 * slot + 1] * f;
-        v += *reinterpret_cast<const f32x4 *>(a.part + slot * D + d) * f;
+    if (there) {
+        if (TILES) {
+            for (int k = 0; k < shares; k++) to = fmaxf(to, ml[2 * (slot0 + int64_t(k) * BM)]);
+        } else {
+            for (int k = threadIdx.x & 63; k < shares; k += 64) to = fmaxf(to, ml[2 * (slot0 + int64_t(k) * BM)]);
+#pragma unroll
+            for (int o = 32; o; o >>= 1) to = fmaxf(to, __shfl_xor(to, o));
+        }
+#pragma unroll 4
+        for (int k = TILES ? 0 : group; k < shares; k += TILES ? 1 : GROUPS) {
+            const int64_t slot = slot0 + int64_t(k) * BM;
+            const float m = ml[2 * slot], f = m == NEG ? 0.0f : __builtin_amdgcn_exp2f(m - to);
+            // a share that saw no finite maximum adds nothing, unless it holds a NaN
+            sum += m == NEG ? ml[2 * slot + 1] : ml[2 * slot + 1] * f;
+            v += *reinterpret_cast<const f32x4 *>(a.part + slot * D + d) * f;
+        }
     }
+    if constexpr (!TILES) {
+        __shared__ float S_v[GROUPS][D], S_l[GROUPS];
+        *reinterpret_cast<f32x4 *>(&S_v[group][d]) = v;
+        if (d == 0) S_l[group] = sum;
+        __syncthreads();
+        if (group > 0) return;
+#pragma unroll
+        for (int g = 1; g < GROUPS; g++) {
+            v += *reinterpret_cast<const f32x4 *>(&S_v[g][d]);
+            sum += S_l[g];
+        }
+    }
+    if (!there) return;
     const int i = (row0 + r) / a.G;
     O *out = static_cast<O *>(a.out) + int64_t(s.start + i) * a.odt + int64_t(h * a.G + row0 + r - i * a.G) * a.odh;
     store4(out + d, sum == 0.0f ? f32x4{0, 0, 0, 0} : v * (1.0f / sum));
@@ -684,17 +776,16 @@ static hipError_t launch_dim(const AttnPlan &p, AttnArgs a, void *workspace, hip
         a.part = reinterpret_cast<float *>(ws);
         const dim3 grid{unsigned(p.few_grid)};
         const unsigned units = unsigned(a.B) * unsigned(a.Hkv);
-        constexpr unsigned ROWS = 1024 / D;
         if (p.few_tiles == 1) {
             k_attn_rows<T, O, D, 1><<<grid, 256, 0, stream>>>(a);
-            if (a.split > 1) k_attn_join<O, D, 16, false><<<dim3(units * ((16 + ROWS - 1) / ROWS)), 256, 0, stream>>>(a);
+            if (a.split > 1) k_attn_join<O, D, 16, false><<<dim3(units * 16), 256, 0, stream>>>(a);
         } else {
             k_attn_rows<T, O, D, 2><<<grid, 256, 0, stream>>>(a);
-            if (a.split > 1) k_attn_join<O, D, 32, false><<<dim3(units * ((32 + ROWS - 1) / ROWS)), 256, 0, stream>>>(a);
+            if (a.split > 1) k_attn_join<O, D, 32, false><<<dim3(units * 32), 256, 0, stream>>>(a);
         }
     }
     if (p.tile_rows) {
-        constexpr int WAVES = D == 256 ? 4 : 8, BM = 32 * WAVES;
+        constexpr int WAVES = D == 128 ? 8 : 4, BM = 32 * WAVES;
         a.split = p.tile_split;
         a.units = int(p.tiles);
         a.part = reinterpret_cast<float *>(ws + p.few_bytes);
@@ -728,6 +819,7 @@ hipError_t launch_attention(const AttnPlan &p, int type, const void *q, int64_t 
     a.T = int(T); a.B = int(B); a.max_q = int(max_q < T ? max_q : T); a.window = window;
     a.scale = float(double(scale) * 1.4426950408889634074);
     a.target = p.target;
+    a.few_rows = p.few_tiles ? kAttnFewRows : 0;
     if (type == TYPE_BF16)
         return out_type == TYPE_F32 ? launch_out<__bf16, float>(p, a, D, workspace, stream)
                                     : launch_out<__bf16, __bf16>(p, a, D, workspace, stream);

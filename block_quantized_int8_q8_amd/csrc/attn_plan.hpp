@@ -151,7 +151,9 @@ inline bool make_plan_attention(int64_t T, int64_t B, int Hq, int Hkv, int D, in
     const int64_t most_rows = max_q * G;
     p->target = 4 * cu_count;
     auto ceil_div = [](int64_t a, int64_t b) { return (a + b - 1) / b; };
-    if (G <= kAttnFewRows || most_rows <= kAttnFewRows) {
+    // a single sequence that may have many rows has them, as a rule: the tile
+    // kernel takes it whatever its rows, and the other need not look
+    if (most_rows <= kAttnFewRows || (G <= kAttnFewRows && B > 1)) {
         p->few_tiles = (most_rows < kAttnFewRows ? most_rows : kAttnFewRows) > 16 ? 2 : 1;
         const int64_t units = B * Hkv;
         int64_t s = ceil_div(4 * int64_t(p->target), units);        // lengths differ: more shares than the device needs
@@ -164,7 +166,7 @@ inline bool make_plan_attention(int64_t T, int64_t B, int Hq, int Hkv, int D, in
         if (p->few_split > 1) p->few_bytes = up256(p->few_grid * 16 * p->few_tiles * (D + 2) * 4);
     }
     if (most_rows > kAttnFewRows) {
-        p->tile_rows = D == 256 ? 128 : 256;
+        p->tile_rows = D == 128 ? 256 : 128;
         p->tiles = T * G / p->tile_rows + (T < B ? T : B);
         if (p->tiles < 1) p->tiles = 1;
         const int64_t units = p->tiles * Hkv;
