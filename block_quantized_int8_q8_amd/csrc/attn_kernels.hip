@@ -186,6 +186,12 @@ constexpr float kSlack = 8.0f;
 constexpr float kNarrowTop = 6.0f, kNarrowSum = 60.0f;
 constexpr float kTop = 6.0f;
 
+// The larger of the values of lanes i and i + 32, in both.
+__device__ __forceinline__ float max_of_halves(float x) {
+    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+
 // --- rows kernel ------------------------------------------------------------
 template <typename T, typename O, int D, int RT>
 __global__ __launch_bounds__(256) void k_attn_rows(AttnArgs a) {
@@ -426,7 +432,8 @@ __global__ __launch_bounds__(64 * WAVES) void k_attn_tile(AttnArgs a) {
     constexpr int LOADS = 8 * D / THREADS;               // 16-byte loads of a lane for 64 keys and 64 values
     constexpr float NEG = -__builtin_inff();
     static_assert(8 * D % (2 * THREADS) == 0, "whole loads of keys and of values");
-    __shared__ __align__(16) uint8_t S_k[2][128 * D], S_v[2][128 * D];
+    constexpr int RING = D == 256 ? 2 : 3;                // buffers of 64 keys, and of 64 values
+    __shared__ __align__(16) uint8_t S_k[RING][128 * D], S_v[RING][128 * D];
     __shared__ __align__(16) float S_ks[4][64], S_lv[4][64], S_rv[4][64];
     const int tid = threadIdx.x, lane = tid & 63, wv = __builtin_amdgcn_readfirstlane(tid >> 6), col = lane & 31, hf = lane >> 5;
     const int h = blockIdx.x % a.Hkv, rest = blockIdx.x / a.Hkv, share = rest / a.units;
@@ -470,7 +477,7 @@ __global__ __launch_bounds__(64 * WAVES) void k_attn_tile(AttnArgs a) {
     // Load i of a wave: 64 chunks of 16 bytes of the keys (of step `step`) or,
     // behind those, of the values (of the step before).
     u32x4 st[LOADS];
-    float st_scale = 0.0f;
+    float st_scale = 0.0f, last_scale = 0x1p-20f;
     int tk = -1, tv = -1;                                 // cache tiles of 16 steps: lane 4 i + j holds 16-key tile j of step i
     int valid = 0;                                        // four bits a step, of four steps: which of its tiles are there
     auto load = [&](int step) __attribute__((always_inline)) {
@@ -491,7 +498,10 @@ __global__ __launch_bounds__(64 * WAVES) void k_attn_tile(AttnArgs a) {
             st[i] = *reinterpret_cast<const u32x4 *>(a.cache + int64_t(t) * TILE + (is_v ? 16 * D : 0) + (at + lane) * 16);
         }
         if (wv < 2) {                                     // wave 0: key scales; wave 1: value scales
-            const int t = __shfl(tk, 4 * (step & 15) + (lane >> 4));
+            const int j = 4 * (step & 15), g = lane >> 4;
+            const int t0 = __builtin_amdgcn_readlane(tk, j), t1 = __builtin_amdgcn_readlane(tk, j + 1);
+            const int t2 = __builtin_amdgcn_readlane(tk, j + 2), t3 = __builtin_amdgcn_readlane(tk, j + 3);
+            const int t = g == 0 ? t0 : g == 1 ? t1 : g == 2 ? t2 : t3;
             st_scale = t >= 0 && begin + 64 * step + lane < end
                            ? reinterpret_cast<const float *>(a.cache + int64_t(t) * TILE + 32 * D)[16 * wv + (lane & 15)]
                            : 0.0f;
@@ -499,18 +509,18 @@ __global__ __launch_bounds__(64 * WAVES) void k_attn_tile(AttnArgs a) {
     };
     // Unit u of the conversion to 16 bits: dword u % 4 of load u / 4.
     uint32_t cw[2][2];
-    auto store = [&](int step, int u) __attribute__((always_inline)) {
+    auto store = [&](int kslot, int vslot, int u) __attribute__((always_inline)) {
         const int i = u / 4, k = u % 4, c = i * THREADS + wv * 64, part = c / D & 3, at = c % D;
         Half<T>::codes(st[i][k], cw[k & 1]);
         if (i < LOADS / 2) {
             // K: lane = (chunk of 16 d, token): fragment (32 keys, 16 d): [half of d][key][8 d]
             const int ch = (at + lane) >> 4, key = 16 * (part & 1) + (lane & 15);
-            uint8_t *p = S_k[step & 1] + ((part >> 1) * KS + ch) * 1024 + key * 16;
+            uint8_t *p = S_k[kslot] + ((part >> 1) * KS + ch) * 1024 + key * 16;
             if (k & 1) *reinterpret_cast<u32x4 *>(p + (k >> 1) * 512) = u32x4{cw[0][0], cw[0][1], cw[1][0], cw[1][1]};
         } else {
             // V: lane = (four tokens g, four d): fragment (16 keys, 32 d): [g & 1][d][g >> 1][4 tokens]
             const int gg = lane >> 4;
-            uint8_t *p = S_v[(step - 1) & 1] + (part * DT + at / 32) * 1024 + (gg & 1) * 512 + (lane & 15) * 16 + (gg >> 1) * 8;
+            uint8_t *p = S_v[vslot] + (part * DT + at / 32) * 1024 + (gg & 1) * 512 + (lane & 15) * 16 + (gg >> 1) * 8;
             *reinterpret_cast<uint2 *>(p + (k >> 1) * 1024 + (k & 1) * 256) = make_uint2(cw[k & 1][0], cw[k & 1][1]);
         }
     };
@@ -518,29 +528,25 @@ __global__ __launch_bounds__(64 * WAVES) void k_attn_tile(AttnArgs a) {
         if (wv == 0) S_ks[step & 3][lane] = st_scale * a.scale;
         if (wv == 1) {
             // A row of zeros has scale 0: any other does for its codes, and
-            // the step's smallest keeps its logarithm among the others.
-            const bool none = st_scale < 0x1p-126f;
-            float least = none ? __builtin_inff() : st_scale;
-#pragma unroll
-            for (int x = 32; x; x >>= 1) least = fminf(least, __shfl_xor(least, x));
-            const float sc = !none ? st_scale : least < __builtin_inff() ? least : 0x1p-20f;
+            // its lane's last keeps the logarithm among the others'.
+            const float sc = st_scale < 0x1p-126f ? last_scale : st_scale;
+            last_scale = sc == sc ? sc : last_scale;
             S_lv[step & 3][lane] = __builtin_amdgcn_logf(sc);
-            S_rv[step & 3][lane] = sc == sc ? 1.0f / sc : 1.0f;       // NaN reaches a row by the logarithm, if it is seen
+            S_rv[step & 3][lane] = sc == sc ? __builtin_amdgcn_rcpf(sc) : 1.0f;       // NaN reaches a row by the logarithm, if it is seen
         }
     };
-    auto store_all = [&](int step) __attribute__((always_inline)) {
+    auto store_all = [&](int step, int kslot, int vslot) __attribute__((always_inline)) {
 #pragma unroll
-        for (int u = 0; u < 4 * LOADS; u++) store(step, u);
+        for (int u = 0; u < 4 * LOADS; u++) store(kslot, vslot, u);
         store_scales(step);
     };
     // Element e of a lane's 32 scores of a step: key 8 (e / 4) + 4 hf + e % 4.
-    auto scaled = [&](float x, float k, float v) __attribute__((always_inline)) { return __builtin_fmaf(x, k, v); };
     auto four = [&](const float (*S)[64], int step, int chunk) __attribute__((always_inline)) {
         return *reinterpret_cast<const f32x4 *>(S[step & 3] + 4 * hf + 8 * chunk);
     };
     // The scores of one step, alone: where a wave's rows begin to see keys.
-    auto first_scores = [&](int step, f32x16 (&sc)[2], float &top) __attribute__((always_inline)) {
-        const uint8_t *K = S_k[step & 1] + lane * 16;
+    auto first_scores = [&](int step, int kslot, f32x16 (&sc)[2], float &top) __attribute__((always_inline)) {
+        const uint8_t *K = S_k[kslot] + lane * 16;
 #pragma unroll
         for (int j = 0; j < 2; j++) {
 #pragma unroll
@@ -554,10 +560,11 @@ __global__ __launch_bounds__(64 * WAVES) void k_attn_tile(AttnArgs a) {
             const f32x4 k4 = four(S_ks, step, ch), v4 = four(S_lv, step, ch);
 #pragma unroll
             for (int y = 0; y < 4; y++) {
-                sc[ch / 4][4 * (ch % 4) + y] = scaled(sc[ch / 4][4 * (ch % 4) + y], k4[y], v4[y]);
+                sc[ch / 4][4 * (ch % 4) + y] = __builtin_fmaf(sc[ch / 4][4 * (ch % 4) + y], k4[y], v4[y]);
                 top = fmaxf(top, sc[ch / 4][4 * (ch % 4) + y]);
             }
         }
+        top = max_of_halves(top);
     };
     // One step.  `sc` holds its scaled scores and `top` their largest, and
     // takes the next step's.  Two runs of D / 8 products each, with the VALU
@@ -565,17 +572,24 @@ __global__ __launch_bounds__(64 * WAVES) void k_attn_tile(AttnArgs a) {
     //   the next step's scores     this step's exponentials
     //   this step's output         the next scores' scales and maximum, and
     //                              the conversion of the step after that
-    // The order is written out and pinned, with fragments four products ahead.
+    // The order is written out and pinned, with fragments four products ahead
+    // (with three buffers, across the barrier too).
+    constexpr int AHEAD = 4;
     float top = NEG;
+    x8 fr[AHEAD];
+    int ring = 0;                                         // of this step's keys and values; the next step's is behind it
+    auto next = [](int x) { return x + 1 == RING ? 0 : x + 1; };
+    auto prefetch = [&](int kslot) __attribute__((always_inline)) {
+#pragma unroll
+        for (int g = 0; g < AHEAD; g++) fr[g] = *reinterpret_cast<const x8 *>(S_k[kslot] + lane * 16 + g * 1024);
+    };
     auto body = [&](int step, f32x16 (&sc)[2]) __attribute__((always_inline)) {
-        constexpr int N = D / 8, E = 32 / N, AHEAD = 4;
-        const int key0 = begin + 64 * step;
+        constexpr int N = D / 8, E = 32 / N;
+        const int key0 = begin + 64 * step, kslot = next(ring), before = RING == 2 ? kslot : next(kslot);
         __syncthreads();
         {
-            const uint8_t *K = S_k[(step + 1) & 1] + lane * 16, *V = S_v[step & 1] + lane * 16;
-            x8 fr[AHEAD];
-#pragma unroll
-            for (int g = 0; g < AHEAD; g++) fr[g] = *reinterpret_cast<const x8 *>(K + g * 1024);
+            const uint8_t *K = S_k[kslot] + lane * 16, *V = S_v[ring] + lane * 16;
+            if (RING == 2) prefetch(kslot);
             f32x4 r4 = four(S_rv, step, 0);
             const int there4 = valid >> 4 * (step & 3) & 15;
             if (!(there4 == 15 && key0 + 63 <= hi_all && key0 > lo_all)) {
@@ -586,9 +600,9 @@ __global__ __launch_bounds__(64 * WAVES) void k_attn_tile(AttnArgs a) {
                     if (!((there4 >> (e / 8) & 1) && key <= pos && key > first)) sc[e / 16][e % 16] = NEG;
                     top = fmaxf(top, sc[e / 16][e % 16]);
                 }
+                top = max_of_halves(top);
             }
-            float want = top - kTop;
-            want = fmaxf(want, __shfl_xor(want, 32));
+            const float want = top - kTop;
             if (__any(want > m + kSlack || (m == NEG && want > NEG))) {
                 const float up = fmaxf(m, want), f = up == NEG ? 1.0f : __builtin_amdgcn_exp2f(m - up);
                 m = up;
@@ -630,10 +644,13 @@ __global__ __launch_bounds__(64 * WAVES) void k_attn_tile(AttnArgs a) {
 #pragma unroll
             for (int g = 0; g < N; g++) {
                 o[g % DT] = Half<T>::mfma32(fr[g % AHEAD], u.p[g / DT], o[g % DT]);
-                if (g + AHEAD < N) fr[g % AHEAD] = *reinterpret_cast<const x8 *>(V + (g + AHEAD) * 1024);
+                if (g + AHEAD < N)
+                    fr[g % AHEAD] = *reinterpret_cast<const x8 *>(V + (g + AHEAD) * 1024);
+                else if (RING > 2)
+                    fr[g % AHEAD] = *reinterpret_cast<const x8 *>(S_k[before] + lane * 16 + (g + AHEAD - N) * 1024);
 #pragma unroll
                 for (int e = g * E; e < g * E + E; e++) {
-                    sc[e / 16][e % 16] = scaled(nx[e / 16][e % 16], k4[e % 4], v4[e % 4]);
+                    sc[e / 16][e % 16] = __builtin_fmaf(nx[e / 16][e % 16], k4[e % 4], v4[e % 4]);
                     top = fmaxf(top, sc[e / 16][e % 16]);
                     if (e % 4 == 3 && e < 31) {
                         k4 = four(S_ks, step + 1, e / 4 + 1);
@@ -641,34 +658,42 @@ __global__ __launch_bounds__(64 * WAVES) void k_attn_tile(AttnArgs a) {
                     }
                 }
                 asm volatile("" : "+v"(top));
-                if ((g + 1) * 4 * LOADS % N == 0) store(step + 2, (g + 1) * 4 * LOADS / N - 1);
+                if ((g + 1) * 4 * LOADS % N == 0) store(ring, before, (g + 1) * 4 * LOADS / N - 1);
                 __builtin_amdgcn_sched_barrier(0);
             }
-            store_scales(step + 2);
+            top = max_of_halves(top);
+            store_scales(step + RING);
         }
-        load(step + 3);
+        load(step + RING + 1);
+        ring = kslot;
     };
+    // A step whose keys the wave's rows do not see.
     auto bring = [&](int step) __attribute__((always_inline)) {
+        const int kslot = next(ring);
         __syncthreads();
-        store_all(step + 2);
-        load(step + 3);
+        store_all(step + RING, ring, RING == 2 ? kslot : next(kslot));
+        load(step + RING + 1);
+        ring = kslot;
     };
     // Buffers: load(s) and store(s) bring the keys of step s and the values of
-    // step s - 1 (past the last step: of tile 0, not used).  In step s the
-    // keys of s + 1 and the values of s are read; those of s + 2 and s + 1
-    // take the places of what step s - 1 has read.
+    // step s - 1 (past the last step: of tile 0, not used).  Step s reads the
+    // keys of s + 1 and the values of s, and stores the keys of s + RING and
+    // the values of s + RING - 1 over those of s and s - 1, which all waves
+    // have read before the barrier that begins it.
     if (steps > 0) {
         f32x16 sc[2];
-        load(0);
-        store_all(0);
-        load(1);
-        store_all(1);
-        load(2);
+#pragma unroll
+        for (int i = 0; i < RING; i++) {
+            load(i);
+            store_all(i, i, (i + RING - 1) % RING);
+        }
+        load(RING);
         __syncthreads();
         int step = 0;
         for (; step < min(from, steps); step++) bring(step);
         if (from <= to) {
-            first_scores(from, sc, top);
+            first_scores(from, ring, sc, top);
+            if (RING > 2) prefetch(next(ring));
             for (; step <= to; step++) body(step, sc);
         }
         for (; step < steps; step++) bring(step);
