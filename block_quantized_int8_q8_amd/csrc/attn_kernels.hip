@@ -577,8 +577,13 @@ __global__ __launch_bounds__(64 * WAVES) void k_attn_tile(AttnArgs a) {
     constexpr int AHEAD = 4;
     float top = NEG;
     x8 fr[AHEAD];
+    f32x4 r4[2];                                          // reciprocals of the values' scales, two fours ahead
     int ring = 0;                                         // of this step's keys and values; the next step's is behind it
     auto next = [](int x) { return x + 1 == RING ? 0 : x + 1; };
+    auto prefetch_r = [&](int step) __attribute__((always_inline)) {
+        r4[0] = four(S_rv, step, 0);
+        r4[1] = four(S_rv, step, 1);
+    };
     auto prefetch = [&](int kslot) __attribute__((always_inline)) {
 #pragma unroll
         for (int g = 0; g < AHEAD; g++) fr[g] = *reinterpret_cast<const x8 *>(S_k[kslot] + lane * 16 + g * 1024);
@@ -590,7 +595,6 @@ __global__ __launch_bounds__(64 * WAVES) void k_attn_tile(AttnArgs a) {
         {
             const uint8_t *K = S_k[kslot] + lane * 16, *V = S_v[ring] + lane * 16;
             if (RING == 2) prefetch(kslot);
-            f32x4 r4 = four(S_rv, step, 0);
             const int there4 = valid >> 4 * (step & 3) & 15;
             if (!(there4 == 15 && key0 + 63 <= hi_all && key0 > lo_all)) {
                 top = NEG;
@@ -616,6 +620,7 @@ __global__ __launch_bounds__(64 * WAVES) void k_attn_tile(AttnArgs a) {
             union { T w[32]; x8 p[4]; } u;
             float pair = 0.0f;
             f32x16 nx[2];
+            f32x4 k4[2], v4[2];
 #pragma unroll
             for (int j = 0; j < 2; j++)
 #pragma unroll
@@ -628,18 +633,24 @@ __global__ __launch_bounds__(64 * WAVES) void k_attn_tile(AttnArgs a) {
 #pragma unroll
                 for (int e = g * E; e < g * E + E; e++) {
                     const float p = __builtin_amdgcn_exp2f(sc[e / 16][e % 16] - ref);
-                    l = __builtin_fmaf(p, r4[e % 4], l);
-                    if (e % 4 == 3 && e < 31) r4 = four(S_rv, step, e / 4 + 1);
+                    l = __builtin_fmaf(p, r4[e / 4 & 1][e % 4], l);
+                    if (e % 4 == 3 && e < 24) r4[e / 4 & 1] = four(S_rv, step, e / 4 + 2);
                     if (e & 1) {
                         u.w[e - 1] = T(pair);
                         u.w[e] = T(p);
                     }
                     pair = p;
                 }
+                if (g == N - 3) {
+#pragma unroll
+                    for (int c = 0; c < 2; c++) {
+                        k4[c] = four(S_ks, step + 1, c);
+                        v4[c] = four(S_lv, step + 1, c);
+                    }
+                }
                 asm volatile("" : "+v"(l));               // summed here: put off, the sums would keep every p in a register
                 __builtin_amdgcn_sched_barrier(0);
             }
-            f32x4 k4 = four(S_ks, step + 1, 0), v4 = four(S_lv, step + 1, 0);
             top = NEG;
 #pragma unroll
             for (int g = 0; g < N; g++) {
@@ -650,13 +661,14 @@ __global__ __launch_bounds__(64 * WAVES) void k_attn_tile(AttnArgs a) {
                     fr[g % AHEAD] = *reinterpret_cast<const x8 *>(S_k[before] + lane * 16 + (g + AHEAD - N) * 1024);
 #pragma unroll
                 for (int e = g * E; e < g * E + E; e++) {
-                    sc[e / 16][e % 16] = __builtin_fmaf(nx[e / 16][e % 16], k4[e % 4], v4[e % 4]);
+                    sc[e / 16][e % 16] = __builtin_fmaf(nx[e / 16][e % 16], k4[e / 4 & 1][e % 4], v4[e / 4 & 1][e % 4]);
                     top = fmaxf(top, sc[e / 16][e % 16]);
-                    if (e % 4 == 3 && e < 31) {
-                        k4 = four(S_ks, step + 1, e / 4 + 1);
-                        v4 = four(S_lv, step + 1, e / 4 + 1);
+                    if (e % 4 == 3 && e < 24) {
+                        k4[e / 4 & 1] = four(S_ks, step + 1, e / 4 + 2);
+                        v4[e / 4 & 1] = four(S_lv, step + 1, e / 4 + 2);
                     }
                 }
+                if (g == N - 1) prefetch_r(step + 1);
                 asm volatile("" : "+v"(top));
                 if ((g + 1) * 4 * LOADS % N == 0) store(ring, before, (g + 1) * 4 * LOADS / N - 1);
                 __builtin_amdgcn_sched_barrier(0);
@@ -694,6 +706,7 @@ __global__ __launch_bounds__(64 * WAVES) void k_attn_tile(AttnArgs a) {
         if (from <= to) {
             first_scores(from, ring, sc, top);
             if (RING > 2) prefetch(next(ring));
+            prefetch_r(from);
             for (; step <= to; step++) body(step, sc);
         }
         for (; step < steps; step++) bring(step);
