@@ -393,35 +393,51 @@ __global__ __launch_bounds__(256) void k_attn_rows(AttnArgs a) {
 // --- tile kernel ------------------------------------------------------------
 
 // The sequence and its tile of BM rows that tile number `tile` of the launch
-// is; false past the last.  Only sequences of many rows have tiles.
+// is; false past the last.  Only sequences of many rows have tiles.  `load`:
+// keys for each of the `target` workgroups that the device runs at once, if
+// all tiles' keys were spread over them evenly.
 template <int BM>
-__device__ __forceinline__ bool find_tile(const AttnArgs &a, int tile, int &b, int &in, int &of) {
+__device__ __forceinline__ bool find_tile(const AttnArgs &a, int tile, int &b, int &in, int &of, float &load) {
     const int lane = threadIdx.x & 63;
     int before = 0;
+    bool found = false;
+    float keys = 0.0f;
     for (int b0 = 0; b0 < a.B; b0 += 64) {
         int n = 0;
+        float mean = 0.0f;
         if (b0 + lane < a.B) {
             const Seq s = sequence(a, b0 + lane);
             if (!has_few_rows(a, s.n)) n = int((int64_t(s.n) * a.G + BM - 1) / BM);
+            mean = fmaxf(float(s.pos0) + 0.5f * float(s.n), 1.0f);
+            if (a.window) mean = fminf(mean, float(a.window) + 0.5f * BM);
         }
+        keys += float(n) * mean;
         const int upto = scan_sum(n);
         const unsigned long long hit = __ballot(before + upto > tile);
-        if (hit) {
+        if (!found && hit) {
             const int i = __builtin_ctzll(hit);
             b = b0 + i;
             of = __builtin_amdgcn_readlane(n, i);
             in = tile - before - (__builtin_amdgcn_readlane(upto, i) - of);
-            return true;
+            found = true;
+            if (a.split == 1) break;
         }
         before += __builtin_amdgcn_readlane(upto, 63);
     }
-    return false;
+    if (a.split > 1) {
+#pragma unroll
+        for (int o = 32; o; o >>= 1) keys += __shfl_xor(keys, o);
+    }
+    // the same in every lane: what follows from it is kept in scalar registers
+    load = __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(keys * float(a.Hkv) / float(a.target))));
+    return found;
 }
 
-// Keys of each share of a tile.
-__device__ __forceinline__ int tile_chunk(const AttnArgs &a, const Range &r) {
-    const int even = (r.end - r.begin + a.split - 1) / a.split;
-    return max((even + 63) & ~63, kAttnTileChunk);
+// Keys of each share of a tile: as many shares as come nearest to the load,
+// all alike.
+__device__ __forceinline__ int tile_chunk(const AttnArgs &a, const Range &r, float load) {
+    const int keys = r.end - r.begin, shares = min(max(int(float(keys) / fmaxf(load, float(kAttnTileChunk)) + 0.5f), 1), a.split);
+    return max(((keys + shares - 1) / shares + 63) & ~63, 64);
 }
 
 template <typename T, typename O, int D, int WAVES>
@@ -438,13 +454,14 @@ __global__ __launch_bounds__(64 * WAVES) void k_attn_tile(AttnArgs a) {
     const int tid = threadIdx.x, lane = tid & 63, wv = __builtin_amdgcn_readfirstlane(tid >> 6), col = lane & 31, hf = lane >> 5;
     const int h = blockIdx.x % a.Hkv, rest = blockIdx.x / a.Hkv, share = rest / a.units;
     int b, in, of;
-    if (!find_tile<BM>(a, rest % a.units, b, in, of)) return;
+    float share_load;
+    if (!find_tile<BM>(a, rest % a.units, b, in, of, share_load)) return;
     b = __builtin_amdgcn_readfirstlane(b);
     in = of - 1 - __builtin_amdgcn_readfirstlane(in);    // the rows with the most keys first
     const Seq s = sequence(a, b);
     const int rows = s.n * a.G, row0 = in * BM;
     const Range all(a, s, row0 / a.G, (min(row0 + BM, rows) - 1) / a.G);
-    const int chunk = tile_chunk(a, all);
+    const int chunk = tile_chunk(a, all, share_load);
     const int begin = all.begin + min(int64_t(share) * chunk, int64_t(all.end - all.begin)), end = min(int64_t(all.end), int64_t(begin) + chunk);
     const bool alone = all.end - all.begin <= chunk;
     if (begin >= end && share > 0) return;
@@ -476,11 +493,14 @@ __global__ __launch_bounds__(64 * WAVES) void k_attn_tile(AttnArgs a) {
 
     // Load i of a wave: 64 chunks of 16 bytes of the keys (of step `step`) or,
     // behind those, of the values (of the step before).
-    u32x4 st[LOADS];
-    float st_scale = 0.0f, last_scale = 0x1p-20f;
+    struct Stage {
+        u32x4 st[LOADS];
+        float scale;                                      // wave 0: of a key; wave 1: of a value
+    };
+    float last_scale = 0x1p-20f;
     int tk = -1, tv = -1;                                 // cache tiles of 16 steps: lane 4 i + j holds 16-key tile j of step i
     int valid = 0;                                        // four bits a step, of four steps: which of its tiles are there
-    auto load = [&](int step) __attribute__((always_inline)) {
+    auto load = [&](int step, Stage &g) __attribute__((always_inline)) {
         tv = tk;
         if ((step & 15) == 0) {
             const int k16 = begin / 16 + 4 * step + lane;
@@ -495,51 +515,54 @@ __global__ __launch_bounds__(64 * WAVES) void k_attn_tile(AttnArgs a) {
             const int part = c / D & 3, at = c % D;
             const int t = max(is_v ? __builtin_amdgcn_readlane(tv, 4 * ((step - 1) & 15) + part)
                                    : __builtin_amdgcn_readlane(tk, 4 * (step & 15) + part), 0);
-            st[i] = *reinterpret_cast<const u32x4 *>(a.cache + int64_t(t) * TILE + (is_v ? 16 * D : 0) + (at + lane) * 16);
+            g.st[i] = *reinterpret_cast<const u32x4 *>(a.cache + int64_t(t) * TILE + (is_v ? 16 * D : 0) + (at + lane) * 16);
         }
         if (wv < 2) {                                     // wave 0: key scales; wave 1: value scales
-            const int j = 4 * (step & 15), g = lane >> 4;
+            const int j = 4 * (step & 15), t16 = lane >> 4;
             const int t0 = __builtin_amdgcn_readlane(tk, j), t1 = __builtin_amdgcn_readlane(tk, j + 1);
             const int t2 = __builtin_amdgcn_readlane(tk, j + 2), t3 = __builtin_amdgcn_readlane(tk, j + 3);
-            const int t = g == 0 ? t0 : g == 1 ? t1 : g == 2 ? t2 : t3;
-            st_scale = t >= 0 && begin + 64 * step + lane < end
+            const int t = t16 == 0 ? t0 : t16 == 1 ? t1 : t16 == 2 ? t2 : t3;
+            g.scale = t >= 0 && begin + 64 * step + lane < end
                            ? reinterpret_cast<const float *>(a.cache + int64_t(t) * TILE + 32 * D)[16 * wv + (lane & 15)]
                            : 0.0f;
         }
     };
+    // The lane's places within what a wave stores, kept in registers (the
+    // compiler would work them out anew in every step).
+    //   K: lane = (chunk of 16 d, token); fragment (32 keys, 16 d): [half of d][key][8 d]
+    //   V: lane = (four tokens g, four d); fragment (16 keys, 32 d): [g & 1][d][g >> 1][4 tokens]
+    int in_k = (lane >> 4) * 1024 + (lane & 15) * 16, in_v = (lane >> 4 & 1) * 512 + (lane & 15) * 16 + (lane >> 5) * 8;
+    asm volatile("" : "+v"(in_k), "+v"(in_v));
     // Unit u of the conversion to 16 bits: dword u % 4 of load u / 4.
     uint32_t cw[2][2];
-    auto store = [&](int kslot, int vslot, int u) __attribute__((always_inline)) {
+    auto store = [&](const Stage &g, int kslot, int vslot, int u) __attribute__((always_inline)) {
         const int i = u / 4, k = u % 4, c = i * THREADS + wv * 64, part = c / D & 3, at = c % D;
-        Half<T>::codes(st[i][k], cw[k & 1]);
+        Half<T>::codes(g.st[i][k], cw[k & 1]);
         if (i < LOADS / 2) {
-            // K: lane = (chunk of 16 d, token): fragment (32 keys, 16 d): [half of d][key][8 d]
-            const int ch = (at + lane) >> 4, key = 16 * (part & 1) + (lane & 15);
-            uint8_t *p = S_k[kslot] + ((part >> 1) * KS + ch) * 1024 + key * 16;
+            uint8_t *p = S_k[kslot] + ((part >> 1) * KS + at / 16) * 1024 + 256 * (part & 1) + in_k;
             if (k & 1) *reinterpret_cast<u32x4 *>(p + (k >> 1) * 512) = u32x4{cw[0][0], cw[0][1], cw[1][0], cw[1][1]};
         } else {
-            // V: lane = (four tokens g, four d): fragment (16 keys, 32 d): [g & 1][d][g >> 1][4 tokens]
-            const int gg = lane >> 4;
-            uint8_t *p = S_v[vslot] + (part * DT + at / 32) * 1024 + (gg & 1) * 512 + (lane & 15) * 16 + (gg >> 1) * 8;
+            uint8_t *p = S_v[vslot] + (part * DT + at / 32) * 1024 + in_v;
             *reinterpret_cast<uint2 *>(p + (k >> 1) * 1024 + (k & 1) * 256) = make_uint2(cw[k & 1][0], cw[k & 1][1]);
         }
     };
-    auto store_scales = [&](int step) __attribute__((always_inline)) {
-        if (wv == 0) S_ks[step & 3][lane] = st_scale * a.scale;
+    auto store_scales = [&](const Stage &g, int step) __attribute__((always_inline)) {
+        if (wv == 0) S_ks[step & 3][lane] = g.scale * a.scale;
         if (wv == 1) {
             // A row of zeros has scale 0: any other does for its codes, and
             // its lane's last keeps the logarithm among the others'.
-            const float sc = st_scale < 0x1p-126f ? last_scale : st_scale;
+            const float sc = g.scale < 0x1p-126f ? last_scale : g.scale;
             last_scale = sc == sc ? sc : last_scale;
             S_lv[step & 3][lane] = __builtin_amdgcn_logf(sc);
             S_rv[step & 3][lane] = sc == sc ? __builtin_amdgcn_rcpf(sc) : 1.0f;       // NaN reaches a row by the logarithm, if it is seen
         }
     };
-    auto store_all = [&](int step, int kslot, int vslot) __attribute__((always_inline)) {
+    auto store_all = [&](const Stage &g, int step, int kslot, int vslot) __attribute__((always_inline)) {
 #pragma unroll
-        for (int u = 0; u < 4 * LOADS; u++) store(kslot, vslot, u);
-        store_scales(step);
+        for (int u = 0; u < 4 * LOADS; u++) store(g, kslot, vslot, u);
+        store_scales(g, step);
     };
+    Stage st;
     // Element e of a lane's 32 scores of a step: key 8 (e / 4) + 4 hf + e % 4.
     auto four = [&](const float (*S)[64], int step, int chunk) __attribute__((always_inline)) {
         return *reinterpret_cast<const f32x4 *>(S[step & 3] + 4 * hf + 8 * chunk);
@@ -670,21 +693,21 @@ __global__ __launch_bounds__(64 * WAVES) void k_attn_tile(AttnArgs a) {
                 }
                 if (g == N - 1) prefetch_r(step + 1);
                 asm volatile("" : "+v"(top));
-                if ((g + 1) * 4 * LOADS % N == 0) store(ring, before, (g + 1) * 4 * LOADS / N - 1);
+                if ((g + 1) * 4 * LOADS % N == 0) store(st, ring, before, (g + 1) * 4 * LOADS / N - 1);
                 __builtin_amdgcn_sched_barrier(0);
             }
             top = max_of_halves(top);
-            store_scales(step + RING);
+            store_scales(st, step + RING);
         }
-        load(step + RING + 1);
+        load(step + RING + 1, st);
         ring = kslot;
     };
     // A step whose keys the wave's rows do not see.
     auto bring = [&](int step) __attribute__((always_inline)) {
         const int kslot = next(ring);
         __syncthreads();
-        store_all(step + RING, ring, RING == 2 ? kslot : next(kslot));
-        load(step + RING + 1);
+        store_all(st, step + RING, ring, RING == 2 ? kslot : next(kslot));
+        load(step + RING + 1, st);
         ring = kslot;
     };
     // Buffers: load(s) and store(s) bring the keys of step s and the values of
@@ -694,12 +717,12 @@ __global__ __launch_bounds__(64 * WAVES) void k_attn_tile(AttnArgs a) {
     // have read before the barrier that begins it.
     if (steps > 0) {
         f32x16 sc[2];
+        Stage fill[RING];
 #pragma unroll
-        for (int i = 0; i < RING; i++) {
-            load(i);
-            store_all(i, i, (i + RING - 1) % RING);
-        }
-        load(RING);
+        for (int i = 0; i < RING; i++) load(i, fill[i]);
+#pragma unroll
+        for (int i = 0; i < RING; i++) store_all(fill[i], i, i, (i + RING - 1) % RING);
+        load(RING, st);
         __syncthreads();
         int step = 0;
         for (; step < min(from, steps); step++) bring(step);
@@ -749,8 +772,9 @@ __global__ __launch_bounds__(256) void k_attn_join(AttnArgs a) {
     constexpr float NEG = -__builtin_inff();
     const int block = blockIdx.x % BLOCKS, unit = blockIdx.x / BLOCKS, h = unit % a.Hkv;
     int b = unit / a.Hkv, in = 0, of = 1;
+    float load = 0.0f;
     if (TILES) {
-        if (!find_tile<BM>(a, unit / a.Hkv, b, in, of)) return;
+        if (!find_tile<BM>(a, unit / a.Hkv, b, in, of, load)) return;
         b = __builtin_amdgcn_readfirstlane(b);
         in = of - 1 - __builtin_amdgcn_readfirstlane(in);
     }
@@ -758,7 +782,7 @@ __global__ __launch_bounds__(256) void k_attn_join(AttnArgs a) {
     const int rows = s.n * a.G, row0 = in * BM, group = threadIdx.x / LANES;
     if (s.n == 0 || has_few_rows(a, s.n) == TILES || row0 + block * ROWS >= rows) return;
     const Range all(a, s, row0 / a.G, (min(row0 + BM, rows) - 1) / a.G);
-    const int chunk = TILES ? tile_chunk(a, all) : few_chunk(a);
+    const int chunk = TILES ? tile_chunk(a, all, load) : few_chunk(a);
     const int shares = (all.end - all.begin + chunk - 1) / chunk;
     const int r = TILES ? block * ROWS + group : block, d = 4 * (threadIdx.x % LANES);
     if (shares <= 1) return;
@@ -810,6 +834,7 @@ static hipError_t launch_dim(const AttnPlan &p, AttnArgs a, void *workspace, hip
     uint8_t *ws = static_cast<uint8_t *>(workspace);
     if (p.few_tiles) {
         a.split = p.few_split;
+        a.target = p.few_target;
         a.units = a.B;
         a.part = reinterpret_cast<float *>(ws);
         const dim3 grid{unsigned(p.few_grid)};
@@ -825,6 +850,7 @@ static hipError_t launch_dim(const AttnPlan &p, AttnArgs a, void *workspace, hip
     if (p.tile_rows) {
         constexpr int WAVES = D == 128 ? 8 : 4, BM = 32 * WAVES;
         a.split = p.tile_split;
+        a.target = p.tile_target;
         a.units = int(p.tiles);
         a.part = reinterpret_cast<float *>(ws + p.few_bytes);
         k_attn_tile<T, O, D, WAVES><<<dim3(unsigned(p.tile_grid)), 64 * WAVES, 0, stream>>>(a);
@@ -856,7 +882,6 @@ hipError_t launch_attention(const AttnPlan &p, int type, const void *q, int64_t 
     a.Hq = Hq; a.Hkv = Hkv; a.G = Hq / Hkv;
     a.T = int(T); a.B = int(B); a.max_q = int(max_q < T ? max_q : T); a.window = window;
     a.scale = float(double(scale) * 1.4426950408889634074);
-    a.target = p.target;
     a.few_rows = p.few_tiles ? kAttnFewRows : 0;
     if (type == TYPE_BF16)
         return out_type == TYPE_F32 ? launch_out<__bf16, float>(p, a, D, workspace, stream)

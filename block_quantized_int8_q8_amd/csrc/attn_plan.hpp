@@ -125,7 +125,7 @@ struct AttnPlan {
     int tile_rows;            // tile kernel: rows per workgroup; 0: not launched
     int tile_split;
     int64_t tiles, tile_grid; // tiles: most row tiles there can be
-    int target;               // workgroups that fill the device
+    int few_target, tile_target;     // workgroups of each that the device runs at once
     int64_t few_bytes, tile_bytes;   // workspace of each, 256-byte multiples
 };
 
@@ -149,16 +149,18 @@ inline bool make_plan_attention(int64_t T, int64_t B, int Hq, int Hkv, int D, in
     const int64_t G = Hq / Hkv, max_keys = max_pages * page;
     if (max_q > T) max_q = T;
     const int64_t most_rows = max_q * G;
-    p->target = 4 * cu_count;
+    p->few_target = 4 * cu_count;
+    p->tile_target = D == 64 ? 2 * cu_count : cu_count;
     auto ceil_div = [](int64_t a, int64_t b) { return (a + b - 1) / b; };
-    // a single sequence that may have many rows has them, as a rule: the tile
-    // kernel takes it whatever its rows, and the other need not look
-    if (most_rows <= kAttnFewRows || (G <= kAttnFewRows && B > 1)) {
+    // Where sequences have many rows on the average, the tile kernel takes the
+    // few-row ones along: they run beside its tiles, the rows kernel would
+    // run before them.
+    if (most_rows <= kAttnFewRows || (G <= kAttnFewRows && T * G < 128 * B)) {
         p->few_tiles = (most_rows < kAttnFewRows ? most_rows : kAttnFewRows) > 16 ? 2 : 1;
         const int64_t units = B * Hkv;
-        int64_t s = ceil_div(4 * int64_t(p->target), units);        // lengths differ: more shares than the device needs
+        int64_t s = ceil_div(4 * int64_t(p->few_target), units);        // lengths differ: more shares than the device needs
         const int64_t most = ceil_div(max_keys + kAttnRowsChunk, kAttnRowsChunk);
-        if (units >= p->target) s = 1;
+        if (units >= p->few_target) s = 1;
         if (s > most) s = most;
         if (s > 512) s = 512;
         p->few_split = int(s < 1 ? 1 : s);
@@ -170,7 +172,7 @@ inline bool make_plan_attention(int64_t T, int64_t B, int Hq, int Hkv, int D, in
         p->tiles = T * G / p->tile_rows + (T < B ? T : B);
         if (p->tiles < 1) p->tiles = 1;
         const int64_t units = p->tiles * Hkv;
-        int64_t s = 2 * cu_count / units;
+        int64_t s = 2 * int64_t(p->tile_target) / units;
         const int64_t most = ceil_div(max_keys + kAttnTileChunk, kAttnTileChunk);
         if (s > most) s = most;
         p->tile_split = int(s < 1 ? 1 : s);
