@@ -615,6 +615,7 @@ __global__ __launch_bounds__(64 * WAVES) void k_attn_tile(AttnArgs a) {
         constexpr int N = D / 8, E = 32 / N;
         const int key0 = begin + 64 * step, kslot = next(ring), before = RING == 2 ? kslot : next(kslot);
         __syncthreads();
+        if (WAVES == 8 && wv >= 4) __builtin_amdgcn_s_setprio(1);
         {
             const uint8_t *K = S_k[kslot] + lane * 16, *V = S_v[ring] + lane * 16;
             if (RING == 2) prefetch(kslot);
@@ -677,6 +678,7 @@ __global__ __launch_bounds__(64 * WAVES) void k_attn_tile(AttnArgs a) {
             top = NEG;
 #pragma unroll
             for (int g = 0; g < N; g++) {
+                if (WAVES == 8 && g == 0) __builtin_amdgcn_s_setprio(0);
                 o[g % DT] = Half<T>::mfma32(fr[g % AHEAD], u.p[g / DT], o[g % DT]);
                 if (g + AHEAD < N)
                     fr[g % AHEAD] = *reinterpret_cast<const x8 *>(V + (g + AHEAD) * 1024);
