@@ -753,9 +753,9 @@ def kv_write(k, v, cache, slots, positions=None, freqs=None, layout=ROPE_HALF, m
     sp = _vector(slots, "slots", c.i32, T, dev)
     pp = fp = None
     rot = 0
+    if (freqs is None) != (positions is None):
+        raise ValueError("freqs and positions go together")
     if freqs is not None:
-        if positions is None:
-            raise ValueError("freqs without positions")
         rot = 2 * freqs.numel()
         fp = _vector(freqs, "freqs", c.f64, freqs.numel(), dev)
         pp = _vector(positions, "positions", c.i32, T, dev)

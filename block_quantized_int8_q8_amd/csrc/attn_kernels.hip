@@ -4,7 +4,8 @@
 //                 query heads): keys and values straight into registers
 //   k_attn_tile   sequences of many rows (a chunk of a prompt): keys and
 //                 values converted once per workgroup, through LDS
-//   k_attn_join   joins the shares of a sequence's keys that either split
+//   k_attn_join_rows, k_attn_join_tiles
+//                 join the shares that they split a sequence's keys into
 //
 // A row is one (new token, query head) pair; the rows of a sequence that read
 // the same key/value head are multiplied together.  With codes c and scales d
@@ -210,6 +211,10 @@ __global__ __launch_bounds__(256) void k_attn_rows(AttnArgs a) {
     if (a.split > 1) chunk = few_chunk(a);
     const int begin = all.begin + min(int64_t(share) * chunk, int64_t(all.end - all.begin)), end = min(int64_t(all.end), int64_t(begin) + chunk);
     const bool alone = all.end - all.begin <= chunk;
+    if (a.split > 1 && share == 0 && threadIdx.x == 0) {                   // for the join: how many shares there are
+        float *ml = a.part + int64_t(a.units) * a.Hkv * a.split * R * (D + 2);
+        reinterpret_cast<int *>(ml)[b * a.Hkv + h] = (all.end - all.begin + chunk - 1) / chunk;
+    }
     if (begin >= end && share > 0) return;
     const bool two = RT > 1 && rows > 16;
 
@@ -763,69 +768,103 @@ __global__ __launch_bounds__(64 * WAVES) void k_attn_tile(AttnArgs a) {
 }
 
 // ---------------------------------------------------------------------------
-// Joins shares: D / 4 lanes a row; the others of a workgroup's lanes take
-// other shares of it (rows kernel: up to hundreds of shares, few rows) or
-// other rows (tile kernel: a few shares, many rows).  Rows whose keys were
-// not split have been written.
+// Joining shares.  Rows whose keys were not split have been written.
 // ---------------------------------------------------------------------------
-template <typename O, int D, int BM, bool TILES>
-__global__ __launch_bounds__(256) void k_attn_join(AttnArgs a) {
-    constexpr int LANES = D / 4, GROUPS = 256 / LANES, ROWS = TILES ? GROUPS : 1, BLOCKS = BM / ROWS;
+struct Joined {
+    f32x4 v;
+    float sum;
+    // One share, for the largest reference `to` of all: one that saw no
+    // finite maximum adds nothing, unless it holds a NaN.
+    __device__ __forceinline__ void add(float m, float l, f32x4 o, float to) {
+        const float f = m == -__builtin_inff() ? 0.0f : __builtin_amdgcn_exp2f(m - to);
+        sum += m == -__builtin_inff() ? l : l * f;
+        v += o * f;
+    }
+    template <typename O>
+    __device__ __forceinline__ void write(const AttnArgs &a, const Seq &s, int h, int r, int d) const {
+        const int i = r / a.G;
+        O *out = static_cast<O *>(a.out) + int64_t(s.start + i) * a.odt + int64_t(h * a.G + r - i * a.G) * a.odh;
+        store4(out + d, sum == 0.0f ? f32x4{0, 0, 0, 0} : v * (1.0f / sum));
+    }
+};
+
+// Rows kernel: up to hundreds of shares of a few rows.  A workgroup a row,
+// D / 4 lanes a share.  The rows kernel left the number of shares, so that
+// nothing here waits for anything but its own loads: the first shares' are
+// under way before their number is known (all lie within the workspace).
+template <typename O, int D, int R>
+__global__ __launch_bounds__(256) void k_attn_join_rows(AttnArgs a, int most_rows) {
+    constexpr int LANES = D / 4, GROUPS = 256 / LANES, EARLY = 4;
     constexpr float NEG = -__builtin_inff();
-    const int block = blockIdx.x % BLOCKS, unit = blockIdx.x / BLOCKS, h = unit % a.Hkv;
-    int b = unit / a.Hkv, in = 0, of = 1;
-    float load = 0.0f;
-    if (TILES) {
-        if (!find_tile<BM>(a, unit / a.Hkv, b, in, of, load)) return;
-        b = __builtin_amdgcn_readfirstlane(b);
-        in = of - 1 - __builtin_amdgcn_readfirstlane(in);
+    __shared__ float S_v[GROUPS][D], S_l[GROUPS];
+    const int r = blockIdx.x % most_rows, unit = blockIdx.x / most_rows, h = unit % a.Hkv, b = unit / a.Hkv;
+    const int group = threadIdx.x / LANES, d = 4 * (threadIdx.x % LANES);
+    const int64_t slot0 = int64_t(unit) * a.split * R + r, slots = int64_t(a.units) * a.Hkv * a.split * R;
+    const float *ml = a.part + slots * D;
+    f32x4 early[EARLY];
+    float early_m[EARLY], early_l[EARLY];
+#pragma unroll
+    for (int j = 0; j < EARLY; j++) {
+        const int64_t slot = slot0 + int64_t(min(group + j * GROUPS, a.split - 1)) * R;
+        early[j] = *reinterpret_cast<const f32x4 *>(a.part + slot * D + d);
+        early_m[j] = ml[2 * slot];
+        early_l[j] = ml[2 * slot + 1];
     }
     const Seq s = sequence(a, b);
-    const int rows = s.n * a.G, row0 = in * BM, group = threadIdx.x / LANES;
-    if (s.n == 0 || has_few_rows(a, s.n) == TILES || row0 + block * ROWS >= rows) return;
-    const Range all(a, s, row0 / a.G, (min(row0 + BM, rows) - 1) / a.G);
-    const int chunk = TILES ? tile_chunk(a, all, load) : few_chunk(a);
-    const int shares = (all.end - all.begin + chunk - 1) / chunk;
-    const int r = TILES ? block * ROWS + group : block, d = 4 * (threadIdx.x % LANES);
+    if (s.n == 0 || !has_few_rows(a, s.n) || r >= s.n * a.G) return;          // no share was written
+    const int shares = reinterpret_cast<const int *>(ml + 2 * slots)[unit];
     if (shares <= 1) return;
-    const bool there = row0 + r < rows;
-    const int64_t slot0 = int64_t(unit) * a.split * BM + r;
-    const float *ml = a.part + int64_t(a.units) * a.Hkv * a.split * BM * D;
-    float to = NEG, sum = 0.0f;
-    f32x4 v = {0, 0, 0, 0};
-    if (there) {
-        if (TILES) {
-            for (int k = 0; k < shares; k++) to = fmaxf(to, ml[2 * (slot0 + int64_t(k) * BM)]);
-        } else {
-            for (int k = threadIdx.x & 63; k < shares; k += 64) to = fmaxf(to, ml[2 * (slot0 + int64_t(k) * BM)]);
+    float to = NEG;
+    for (int k = threadIdx.x & 63; k < shares; k += 64) to = fmaxf(to, ml[2 * (slot0 + int64_t(k) * R)]);
 #pragma unroll
-            for (int o = 32; o; o >>= 1) to = fmaxf(to, __shfl_xor(to, o));
-        }
+    for (int o = 32; o; o >>= 1) to = fmaxf(to, __shfl_xor(to, o));
+    Joined j{{0, 0, 0, 0}, 0.0f};
+#pragma unroll
+    for (int e = 0; e < EARLY; e++)
+        if (group + e * GROUPS < shares) j.add(early_m[e], early_l[e], early[e], to);
 #pragma unroll 4
-        for (int k = TILES ? 0 : group; k < shares; k += TILES ? 1 : GROUPS) {
-            const int64_t slot = slot0 + int64_t(k) * BM;
-            const float m = ml[2 * slot], f = m == NEG ? 0.0f : __builtin_amdgcn_exp2f(m - to);
-            // a share that saw no finite maximum adds nothing, unless it holds a NaN
-            sum += m == NEG ? ml[2 * slot + 1] : ml[2 * slot + 1] * f;
-            v += *reinterpret_cast<const f32x4 *>(a.part + slot * D + d) * f;
-        }
+    for (int k = group + EARLY * GROUPS; k < shares; k += GROUPS) {
+        const int64_t slot = slot0 + int64_t(k) * R;
+        j.add(ml[2 * slot], ml[2 * slot + 1], *reinterpret_cast<const f32x4 *>(a.part + slot * D + d), to);
     }
-    if constexpr (!TILES) {
-        __shared__ float S_v[GROUPS][D], S_l[GROUPS];
-        *reinterpret_cast<f32x4 *>(&S_v[group][d]) = v;
-        if (d == 0) S_l[group] = sum;
-        __syncthreads();
-        if (group > 0) return;
+    *reinterpret_cast<f32x4 *>(&S_v[group][d]) = j.v;
+    if (d == 0) S_l[group] = j.sum;
+    __syncthreads();
+    if (group > 0) return;
 #pragma unroll
-        for (int g = 1; g < GROUPS; g++) {
-            v += *reinterpret_cast<const f32x4 *>(&S_v[g][d]);
-            sum += S_l[g];
-        }
+    for (int g = 1; g < GROUPS; g++) {
+        j.v += *reinterpret_cast<const f32x4 *>(&S_v[g][d]);
+        j.sum += S_l[g];
     }
-    if (!there) return;
-    const int i = (row0 + r) / a.G;
-    O *out = static_cast<O *>(a.out) + int64_t(s.start + i) * a.odt + int64_t(h * a.G + row0 + r - i * a.G) * a.odh;
-    store4(out + d, sum == 0.0f ? f32x4{0, 0, 0, 0} : v * (1.0f / sum));
+    j.write<O>(a, s, h, r, d);
+}
+
+// Tile kernel: a few shares of many rows.  D / 4 lanes a row.
+template <typename O, int D, int BM>
+__global__ __launch_bounds__(256) void k_attn_join_tiles(AttnArgs a) {
+    constexpr int LANES = D / 4, ROWS = 256 / LANES, BLOCKS = BM / ROWS;
+    const int block = blockIdx.x % BLOCKS, unit = blockIdx.x / BLOCKS, h = unit % a.Hkv;
+    int b, in, of;
+    float load;
+    if (!find_tile<BM>(a, unit / a.Hkv, b, in, of, load)) return;
+    b = __builtin_amdgcn_readfirstlane(b);
+    in = of - 1 - __builtin_amdgcn_readfirstlane(in);
+    const Seq s = sequence(a, b);
+    const int rows = s.n * a.G, row0 = in * BM, slot_r = block * ROWS + threadIdx.x / LANES, r = row0 + slot_r, d = 4 * (threadIdx.x % LANES);
+    const Range all(a, s, row0 / a.G, (min(row0 + BM, rows) - 1) / a.G);
+    const int chunk = tile_chunk(a, all, load), shares = (all.end - all.begin + chunk - 1) / chunk;
+    if (shares <= 1 || r >= rows) return;
+    const int64_t slot0 = int64_t(unit) * a.split * BM + slot_r;
+    const float *ml = a.part + int64_t(a.units) * a.Hkv * a.split * BM * D;
+    float to = -__builtin_inff();
+    for (int k = 0; k < shares; k++) to = fmaxf(to, ml[2 * (slot0 + int64_t(k) * BM)]);
+    Joined j{{0, 0, 0, 0}, 0.0f};
+#pragma unroll 4
+    for (int k = 0; k < shares; k++) {
+        const int64_t slot = slot0 + int64_t(k) * BM;
+        j.add(ml[2 * slot], ml[2 * slot + 1], *reinterpret_cast<const f32x4 *>(a.part + slot * D + d), to);
+    }
+    j.write<O>(a, s, h, r, d);
 }
 
 // ---------------------------------------------------------------------------
@@ -840,13 +879,14 @@ static hipError_t launch_dim(const AttnPlan &p, AttnArgs a, void *workspace, hip
         a.units = a.B;
         a.part = reinterpret_cast<float *>(ws);
         const dim3 grid{unsigned(p.few_grid)};
-        const unsigned units = unsigned(a.B) * unsigned(a.Hkv);
+        const int most_rows = int(std::min(int64_t(a.max_q) * a.G, int64_t(kAttnFewRows)));
+        const dim3 rows{unsigned(a.B) * unsigned(a.Hkv) * unsigned(most_rows)};
         if (p.few_tiles == 1) {
             k_attn_rows<T, O, D, 1><<<grid, 256, 0, stream>>>(a);
-            if (a.split > 1) k_attn_join<O, D, 16, false><<<dim3(units * 16), 256, 0, stream>>>(a);
+            if (a.split > 1) k_attn_join_rows<O, D, 16><<<rows, 256, 0, stream>>>(a, most_rows);
         } else {
             k_attn_rows<T, O, D, 2><<<grid, 256, 0, stream>>>(a);
-            if (a.split > 1) k_attn_join<O, D, 32, false><<<dim3(units * 32), 256, 0, stream>>>(a);
+            if (a.split > 1) k_attn_join_rows<O, D, 32><<<rows, 256, 0, stream>>>(a, most_rows);
         }
     }
     if (p.tile_rows) {
@@ -857,7 +897,7 @@ static hipError_t launch_dim(const AttnPlan &p, AttnArgs a, void *workspace, hip
         a.part = reinterpret_cast<float *>(ws + p.few_bytes);
         k_attn_tile<T, O, D, WAVES><<<dim3(unsigned(p.tile_grid)), 64 * WAVES, 0, stream>>>(a);
         if (a.split > 1)
-            k_attn_join<O, D, BM, true><<<dim3(unsigned(p.tiles) * unsigned(a.Hkv) * (BM * D / 1024)), 256, 0, stream>>>(a);
+            k_attn_join_tiles<O, D, BM><<<dim3(unsigned(p.tiles) * unsigned(a.Hkv) * (BM * D / 1024)), 256, 0, stream>>>(a);
     }
     return hipGetLastError();
 }

@@ -149,7 +149,7 @@ inline bool make_plan_attention(int64_t T, int64_t B, int Hq, int Hkv, int D, in
     const int64_t G = Hq / Hkv, max_keys = max_pages * page;
     if (max_q > T) max_q = T;
     const int64_t most_rows = max_q * G;
-    p->few_target = 4 * cu_count;
+    p->few_target = 3 * cu_count;
     p->tile_target = D == 64 ? 2 * cu_count : cu_count;
     auto ceil_div = [](int64_t a, int64_t b) { return (a + b - 1) / b; };
     // Where sequences have many rows on the average, the tile kernel takes the
@@ -165,7 +165,7 @@ inline bool make_plan_attention(int64_t T, int64_t B, int Hq, int Hkv, int D, in
         if (s > 512) s = 512;
         p->few_split = int(s < 1 ? 1 : s);
         p->few_grid = units * p->few_split;
-        if (p->few_split > 1) p->few_bytes = up256(p->few_grid * 16 * p->few_tiles * (D + 2) * 4);
+        if (p->few_split > 1) p->few_bytes = up256(p->few_grid * 16 * p->few_tiles * (D + 2) * 4 + units * 4);
     }
     if (most_rows > kAttnFewRows) {
         p->tile_rows = D == 128 ? 256 : 128;
@@ -179,7 +179,8 @@ inline bool make_plan_attention(int64_t T, int64_t B, int Hq, int Hkv, int D, in
         p->tile_grid = units * p->tile_split;
         if (p->tile_split > 1) p->tile_bytes = up256(p->tile_grid * p->tile_rows * (D + 2) * 4);
     }
-    if (p->few_grid >= (int64_t(1) << 23) || p->tile_grid >= (int64_t(1) << 23)) {
+    // a launch holds fewer than 2^32 threads
+    if (p->few_grid >= (int64_t(1) << 23) || p->tile_grid >= (int64_t(1) << 22)) {
         std::snprintf(why, len, "too many workgroups for one launch");
         return false;
     }

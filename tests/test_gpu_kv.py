@@ -336,6 +336,7 @@ def test_binding_refuses():
         (lambda: mmq.kv_write(x, x[:2], cache, i3), "v:"), (lambda: mmq.kv_write(x, x.half(), cache, i3), "v:"),
         (lambda: mmq.kv_write(x[:, :1], x[:, :1], cache, i3), "heads"), (lambda: mmq.kv_write(x, x, cache[:, :, :-8], i3), "cache"),
         (lambda: mmq.kv_write(x, x, cache, i3[:1]), "slots"), (lambda: mmq.kv_write(x, x, cache, i3, freqs=f), "positions"),
+        (lambda: mmq.kv_write(x, x, cache, i3, positions=i3), "positions"),
         (lambda: mmq.kv_read(cache, i3, 128), "cache"), (lambda: mmq.kv_read(cache, i3, 64, dtype=F32, k=x), "k:"),
         (lambda: mmq.attention_i8(x.float(), cache, table, lens, off), "bf16 or fp16"),
         (lambda: mmq.attention_i8(x, cache, table[0], lens, off), "page_table"),
