@@ -175,17 +175,21 @@ __device__ __forceinline__ int few_chunk(const AttnArgs &a) {
 // ---------------------------------------------------------------------------
 // Softmax of the transposed scores in a lane's registers.
 //
-// Scores are in units of log2.  p = 2^(t - m) for a running reference m of
-// the row.  The second product's operand p * dv has the exponents of its type:
-// in bf16 any m near the maximum of t will do; in fp16 (NARROW) m is taken so
-// that the largest p * dv is between 2^6 and 2^14, whatever the size of dv:
-// m = max(t + log2 dv) - 6, but not so low that the sum of p leaves fp32
-// (m >= max(t) - 60: where that binds, the output is below 2^-47).  References
-// move up only, and only when a new maximum lies more than 2^8 above.
+// Scores t are in units of log2, p = 2^(t - m) for a running reference m of
+// the row, which moves up only, and only when a new maximum lies more than
+// 2^8 above.  The second product's operand is p * dv in 16 bits.  In fp16 its
+// exponents end at 15 and -24, so there m must follow t + log2 dv: the largest
+// p * dv lies between 2^6 and 2^14, whatever the size of dv.
+//   Tile kernel: the scale goes into the exponent, p' = 2^(t + log2 dv - m) =
+// p * dv, one FMA on the product where two multiplications were (the sum of
+// p takes p' / dv), and m = max(t + log2 dv) - 6 for both types.
+//   Rows kernel, a few scores a lane: p and p * dv are formed apart.  In bf16
+// m = max(t); in fp16 (NARROW) m = max(t + log2 dv) - 6, but not so low that
+// the sum of p leaves fp32 (m >= max(t) - 60: where that binds, the output is
+// below 2^-47).
 // ---------------------------------------------------------------------------
 constexpr float kSlack = 8.0f;
-constexpr float kNarrowTop = 6.0f, kNarrowSum = 60.0f;
-constexpr float kTop = 6.0f;
+constexpr float kTop = 6.0f, kNarrowSum = 60.0f;
 
 // The larger of the values of lanes i and i + 32, in both.
 __device__ __forceinline__ float max_of_halves(float x) {
@@ -301,7 +305,7 @@ __global__ __launch_bounds__(256) void k_attn_rows(AttnArgs a) {
                     top = fmaxf(top, t[j][i]);
                     if (Half<T>::NARROW) low = fmaxf(low, seen[j][i] ? t[j][i] + __builtin_amdgcn_logf(vs[j][i]) : NEG);
                 }
-            float want = Half<T>::NARROW ? fmaxf(low - kNarrowTop, top - kNarrowSum) : top;
+            float want = Half<T>::NARROW ? fmaxf(low - kTop, top - kNarrowSum) : top;
             want = fmaxf(want, __shfl_xor(want, 16));
             want = fmaxf(want, __shfl_xor(want, 32));
             if (__any(want > m[rb] + kSlack || (m[rb] == NEG && want > NEG))) {
@@ -502,7 +506,7 @@ __global__ __launch_bounds__(64 * WAVES) void k_attn_tile(AttnArgs a) {
         u32x4 st[LOADS];
         float scale;                                      // wave 0: of a key; wave 1: of a value
     };
-    float last_scale = 0x1p-20f;
+    float last_scale = 1.0f;
     int tk = -1, tv = -1;                                 // cache tiles of 16 steps: lane 4 i + j holds 16-key tile j of step i
     int valid = 0;                                        // four bits a step, of four steps: which of its tiles are there
     auto load = [&](int step, Stage &g) __attribute__((always_inline)) {
@@ -554,10 +558,14 @@ __global__ __launch_bounds__(64 * WAVES) void k_attn_tile(AttnArgs a) {
     auto store_scales = [&](const Stage &g, int step) __attribute__((always_inline)) {
         if (wv == 0) S_ks[step & 3][lane] = g.scale * a.scale;
         if (wv == 1) {
-            // A row of zeros has scale 0: any other does for its codes, and
-            // its lane's last keeps the logarithm among the others'.
-            const float sc = g.scale < 0x1p-126f ? last_scale : g.scale;
-            last_scale = sc == sc ? sc : last_scale;
+            // A row of zeros has scale 0.  Any other does for its codes: 2^-40
+            // of its lane's last, 1 at most, which keeps its weight for the
+            // sum and leaves the reference to the rows that are not zero.
+            // Below 2^-100 the exponential would lose the row's weight with
+            // its value: there a scale counts as 2^-100.
+            const float stand_in = fmaxf(last_scale * 0x1p-40f, 0x1p-100f);
+            const float sc = g.scale >= 0x1p-100f || g.scale != g.scale ? g.scale : g.scale == 0.0f ? stand_in : 0x1p-100f;
+            if (g.scale >= 0x1p-100f) last_scale = fminf(g.scale, 1.0f);
             S_lv[step & 3][lane] = __builtin_amdgcn_logf(sc);
             S_rv[step & 3][lane] = sc == sc ? __builtin_amdgcn_rcpf(sc) : 1.0f;       // NaN reaches a row by the logarithm, if it is seen
         }

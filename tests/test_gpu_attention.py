@@ -17,11 +17,13 @@ magnitudes in the same units, N keys:
     the terms of second order.
   - the weight of a value: p_t times its scale, u, rounded to q's type, h
     (fp16: below 2^-14 by 2^-25 at most; its largest is at least 2^6, so that
-    is 2^-31 of the largest product of weight and scale, times codes of 127).
+    is 2^-31 of the largest product of weight and scale, times codes of 127; a
+    row of zeros takes part in that largest with a scale of at most 2^-40).
   - numbers below 2^-126 may be taken as 0, by exp2 and by the matrix core: a
     weight of p_t / p_max below 2^-118 (the reference stands up to 2^8 from the
     maximum) is lost, N 2^-118 of the largest value at most (a first form
     without this term was off by 4e-40 where one weight was all there was).
+    A value's scale below 2^-100 may count as that: 127 * 2^-100 < 2^-93.
   - sums over N keys: N u, twice for the matrix core, of the magnitudes; the
     shares' factors and the quotient, 8u.
   - the output's own rounding."""
@@ -133,9 +135,9 @@ def reference(bt, scale, window=0, table=None):
             N = length
             mag = w @ V.abs()
             bound = 2 * ((w * eps) @ V.abs() + (w * eps).sum(1, keepdim=True) * wv.abs()) + (h16 * (1 + 2 * h16) + 3 * N * U + 9 * U) * mag \
-                + N * U * wv.abs() + N * 2.0 ** -118 * V.abs().amax()
+                + N * U * wv.abs() + N * 2.0 ** -118 * V.abs().amax() + 2.0 ** -93
             if bt.q.dtype == F16:
-                bound = bound + N * 2.0 ** -24 * (w * torch.where(seen, w_d[None], 0.0)).amax(1, keepdim=True)
+                bound = bound + N * 2.0 ** -24 * ((w * torch.where(seen, w_d[None], 0.0)).amax(1, keepdim=True) + 2.0 ** -40)
             o[:, h], e[:, h] = wv, bound
         outs.append(o)
         bounds.append(e)
@@ -328,6 +330,38 @@ def test_zero_keys_and_values():
         assert bool((bt.run() == 0).all())
         bt = Batch([40, 1], [100, 300], 4, 2, 64, 16, t, k=zero)
         check(bt, bt.run())
+
+
+@pytest.mark.parametrize("t", [BF16, F16])
+@pytest.mark.parametrize("small", [0.0, 1e-37, 1e-30, 1e-6])
+@pytest.mark.parametrize("new,lens", [([1], [700]), ([100], [700]), ([200, 1], [200, 90])])
+def test_rows_of_zeros_and_tiny_values_keep_their_weight(new, lens, small, t):
+    """Values that are zero, or next to nothing, at every third key, at runs of 64 keys and at the keys that weigh most:
+    they add nothing to the output and all of their weight to the sum."""
+    def v(total):
+        x = heads(total, 2, 64, F32, 31)
+        i = torch.arange(total, device=DEV)
+        x[(i % 3 == 1) | (i // 64 % 4 == 2)] *= small
+        return x
+
+    def k(total):
+        x = heads(total, 2, 64, F32, 32)
+        x[torch.arange(total, device=DEV) % 3 == 1] *= 3.0
+        return x
+    bt = Batch(new, lens, 8, 2, 64, 16, t, k=k, v=v)
+    check(bt, bt.run(dtype=F32))
+    check(bt, bt.run())
+    bt = Batch(new, lens, 8, 2, 64, 16, t, k=k, v=lambda total: heads(total, 2, 64, F32, 33) * small)
+    check(bt, bt.run(dtype=F32))
+
+
+@pytest.mark.parametrize("t", [BF16, F16])
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("new,lens,window", [([2500], [2500], 0), ([1300, 900], [3300, 900], 0), ([2100], [4000], 1500)])
+def test_long_chunks(new, lens, window, D, t):
+    """Workgroups that walk more steps than they look up pages for at once."""
+    bt = Batch(new, lens, 16, 8, D, 16 if D == 64 else 32, t, seed=13)
+    check(bt, bt.run(window=window), window=window)
 
 
 @pytest.mark.parametrize("scale", [0.0, -0.3, 1.0, 5.0])

@@ -56,7 +56,9 @@ def close(got, y, bound):
 
 
 ROPES = [(1, 1, 64, 64), (1, 28, 128, 128), (3, 5, 128, 32), (7, 4, 256, 256), (64, 28, 128, 128), (65, 3, 96, 96), (33, 2, 80, 40),
-         (1025, 4, 128, 128), (1030, 3, 64, 20), (1027, 1, 8, 6), (5, 9, 512, 512), (17, 6, 40, 2), (1100, 2, 256, 64), (9, 1, 16, 16)]
+         (1025, 4, 128, 128), (1030, 3, 64, 20), (1027, 1, 8, 6), (5, 9, 512, 512), (17, 6, 40, 2), (1100, 2, 256, 64), (9, 1, 16, 16),
+         # four tokens a workgroup
+         (4100, 3, 128, 128), (4097, 2, 64, 20), (4099, 1, 80, 40), (4111, 5, 64, 32), (5000, 2, 256, 256), (4098, 2, 8, 8)]
 
 
 @pytest.mark.parametrize("layout", [mmq.ROPE_HALF, mmq.ROPE_INTERLEAVED])
@@ -80,7 +82,7 @@ def test_rope(T, H, D, rot, layout):
 def test_rope_strides_and_in_place(t, layout):
     """A slice of a fused product's rows turned in place, [H, T, D] in memory, and one head for all: what lies between
     is not touched, and all give the same bits."""
-    for T in (6, 1300):
+    for T in (6, 1300, 4203):
         H, D = 5, 64
         freqs, _ = mmq.rope_frequencies(48)
         freqs, positions = freqs.to(DEV), torch.arange(T, dtype=torch.int32, device=DEV) * 3
@@ -136,7 +138,9 @@ def test_frequencies_against_the_formulas():
 # cache
 # ---------------------------------------------------------------------------
 CACHES = [(1, 1, 64, 16), (1, 4, 128, 16), (5, 3, 256, 32), (64, 4, 128, 64), (70, 8, 64, 128), (1024, 2, 128, 16), (1111, 1, 64, 256),
-          (1030, 5, 256, 64)]
+          (1030, 5, 256, 64),
+          # sixteen tokens a workgroup
+          (4099, 2, 64, 16), (2061, 5, 128, 64), (1501, 8, 256, 32), (4100, 1, 128, 16), (2050, 7, 64, 256), (5000, 3, 256, 16)]
 
 
 @pytest.mark.parametrize("t", TYPES)
@@ -162,9 +166,35 @@ def test_write_and_read(T, H, D, page, t):
         assert read.dtype == t and torch.equal(read.cpu(), (want.float() * scale[..., None]).to(t))
 
 
+@pytest.mark.parametrize("t", TYPES)
+@pytest.mark.parametrize("first", [0, 1, 2, 3, 7])
+@pytest.mark.parametrize("H,D", [(4, 128), (8, 64), (3, 256)])
+def test_write_consecutive_slots_from_any_place(H, D, first, t):
+    """A prompt's slots in a row, from any place of a page, with a jump and a token that is passed over among them, and
+    a batch whose sequences begin at their own places."""
+    T = 4099
+    n_pages = (T + 200) // 32 + 1
+    slots = torch.arange(first, first + T, dtype=torch.int32)
+    slots[1000:] += 5
+    slots[2000:] += 50
+    slots[77] = -1
+    slots[3001:3400] = slots[3001:3400].flip(0)
+    cache = mmq.kv_cache(n_pages, 32, H, D, device=DEV)
+    cache.fill_(0x11)
+    before = kvcache.unpack(cache.cpu(), D)
+    k, v = rand((T, H, D), t, 1), rand((T, H, D), t, 2)
+    mmq.kv_write(k.to(DEV), v.to(DEV), cache, slots.to(DEV))
+    kept = slots >= 0
+    for x, (codes, d), (codes0, d0) in zip((k, v), kvcache.unpack(cache.cpu(), D), before):
+        want, scale = kvcache.quantize_rows(x)
+        codes0[slots[kept].long()], d0[slots[kept].long()] = want[kept], scale[kept]
+        assert torch.equal(codes, codes0) and torch.equal(d.view(torch.int32), d0.view(torch.int32))
+
+
 @pytest.mark.parametrize("layout", [mmq.ROPE_HALF, mmq.ROPE_INTERLEAVED])
 @pytest.mark.parametrize("T,H,D,rot,t", [(1, 4, 128, 128, BF16), (9, 2, 64, 20, F32), (1031, 3, 128, 32, F16), (1050, 1, 256, 256, F32),
-                                         (40, 8, 256, 128, BF16)])
+                                         (40, 8, 256, 128, BF16), (4101, 2, 128, 128, BF16), (1503, 7, 64, 20, F32),
+                                         (1499, 8, 256, 64, F16), (4100, 1, 128, 6, BF16)])
 def test_write_turns_keys(T, H, D, rot, t, layout):
     freqs, m = mmq.rope_frequencies(rot, base=1e6, scaling="yarn", factor=8.0, original=32768)
     positions = torch.arange(900000, 900000 + T, dtype=torch.int32)
@@ -186,8 +216,8 @@ def test_write_turns_keys(T, H, D, rot, t, layout):
 
 
 def test_write_passes_over_slots_outside_and_read_leaves_their_rows():
-    T, H, D, page, n_pages = 9, 2, 64, 16, 2
-    for T in (9, 1500):
+    H, D, page = 2, 64, 16
+    for T in (9, 1500, 4503):
         n_pages = T // 16 + 1
         cache = mmq.kv_cache(n_pages, page, H, D, device=DEV)
         cache.fill_(0x5a)
