@@ -404,7 +404,9 @@ __global__ __launch_bounds__(256) void k_attn_rows(AttnArgs a) {
 // The sequence and its tile of BM rows that tile number `tile` of the launch
 // is; false past the last.  Only sequences of many rows have tiles.  `load`:
 // keys for each of the `target` workgroups that the device runs at once, if
-// all tiles' keys were spread over them evenly.
+// all tiles' keys were spread over them evenly.  Sequences are taken 64 at a
+// time, up to 256 of them those whose tiles see the most keys first, so that
+// the last workgroups to start are short ones.
 template <int BM>
 __device__ __forceinline__ bool find_tile(const AttnArgs &a, int tile, int &b, int &in, int &of, float &load) {
     const int lane = threadIdx.x & 63;
@@ -412,20 +414,34 @@ __device__ __forceinline__ bool find_tile(const AttnArgs &a, int tile, int &b, i
     bool found = false;
     float keys = 0.0f;
     for (int b0 = 0; b0 < a.B; b0 += 64) {
-        int n = 0;
+        int n = 0, most = -1, at = lane;
         float mean = 0.0f;
         if (b0 + lane < a.B) {
             const Seq s = sequence(a, b0 + lane);
             if (!has_few_rows(a, s.n)) n = int((int64_t(s.n) * a.G + BM - 1) / BM);
             mean = fmaxf(float(s.pos0) + 0.5f * float(s.n), 1.0f);
-            if (a.window) mean = fminf(mean, float(a.window) + 0.5f * BM);
+            most = s.len;
+            if (a.window) {
+                mean = fminf(mean, float(a.window) + 0.5f * BM);
+                most = min(most, a.window);
+            }
         }
         keys += float(n) * mean;
+        const int here = min(a.B - b0, 64);
+        if (here > 1 && a.B <= 256) {                     // (more have many workgroups each, and the sort its cost)
+            int rank = 0;
+            for (int j = 0; j < here; j++) {
+                const int other = __builtin_amdgcn_readlane(most, j);
+                rank += other > most || (other == most && j < lane);
+            }
+            n = __builtin_amdgcn_ds_permute(4 * rank, n);            // lanes past the last: most = -1, behind all
+            at = __builtin_amdgcn_ds_permute(4 * rank, lane);
+        }
         const int upto = scan_sum(n);
         const unsigned long long hit = __ballot(before + upto > tile);
         if (!found && hit) {
             const int i = __builtin_ctzll(hit);
-            b = b0 + i;
+            b = b0 + __builtin_amdgcn_readlane(at, i);
             of = __builtin_amdgcn_readlane(n, i);
             in = tile - before - (__builtin_amdgcn_readlane(upto, i) - of);
             found = true;
