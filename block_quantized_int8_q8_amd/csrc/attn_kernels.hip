@@ -198,6 +198,17 @@ __device__ __forceinline__ float max_of_halves(float x) {
 }
 
 // --- rows kernel ------------------------------------------------------------
+//
+// Bound by the cache's bytes.  A workgroup is one sequence and key/value head
+// (and a share of its keys); each of its four waves takes 32 keys at a time
+// straight into the operands' registers: the cache's layout is that of the
+// matrix instruction's fragments, 1 KiB a load, no LDS and no wait for
+// another wave before the end.  Rows are the other operand, 16 or 32 of them,
+// so that a group of query heads reads its keys once.
+//   64 sequences of 2K to 16K keys, 28 on 4 heads of 128: 101 us for 506 MB =
+//   5.0 TB/s (a copy moves 5.12), and 6.6 for the join of its shares
+//   one sequence of 256K keys, 32 on 4 heads: 60 us for 277 MB, join 8
+//   one of 2011 keys: 5.9 us, a chain of offsets, pages, keys; join 3.8
 template <typename T, typename O, int D, int RT>
 __global__ __launch_bounds__(256) void k_attn_rows(AttnArgs a) {
     typedef typename Half<T>::x8 x8;
@@ -400,7 +411,26 @@ __global__ __launch_bounds__(256) void k_attn_rows(AttnArgs a) {
 }
 
 // --- tile kernel ------------------------------------------------------------
-
+//
+// A workgroup is 256 rows (128 for D = 64 and 256) of one sequence and head,
+// 32 a wave, and walks the keys 64 at a time.  Codes come through registers,
+// are converted to 16 bits once per workgroup (two fragments' worth a wave)
+// and lie in LDS in the order of the matrix instruction's fragments: every
+// read is 1 KiB in a row.
+//
+// What bounds it (8192 x 8192 causal, 28 on 4 heads of 128, bf16: 514 us = 936
+// TFLOP/s; a large library product reaches 1233): VALU and matrix core
+// together.  A step of a wave is 32 products of 32 cycles and about 260 other
+// vector instructions, 32 of them exponentials and 48 conversions; a product costs the VALU two to three instructions' time.  The matrix cores
+// are busy 41 % of the time at 1.9 GHz, where the power limit holds the clock.
+// Steps that led here, us: scores, softmax and output one after the other
+// 677; next scores behind this step's exponentials, scales behind the
+// output's products, values' scales in the exponent 543; three buffers,
+// fragments read across the barrier 536; no wave with more to do than the
+// others before the barrier 518; younger waves first in the first half 514.
+// Tried and not kept: 128 rows and two workgroups a CU (594: codes are
+// converted twice as often), loads two steps ahead (546), scales loaded by
+// all waves (546).
 // The sequence and its tile of BM rows that tile number `tile` of the launch
 // is; false past the last.  Only sequences of many rows have tiles.  `load`:
 // keys for each of the `target` workgroups that the device runs at once, if
@@ -644,6 +674,7 @@ __global__ __launch_bounds__(64 * WAVES) void k_attn_tile(AttnArgs a) {
         constexpr int N = D / 8, E = 32 / N;
         const int key0 = begin + 64 * step, kslot = next(ring), before = RING == 2 ? kslot : next(kslot);
         __syncthreads();
+        // of a SIMD's two waves the older runs first and then waits, ~1000 of a step's 4400 cycles: the younger first for half
         if (WAVES == 8 && wv >= 4) __builtin_amdgcn_s_setprio(1);
         {
             const uint8_t *K = S_k[kslot] + lane * 16, *V = S_v[ring] + lane * 16;

@@ -113,7 +113,9 @@ inline const char *check_rope(int D, int rot, int layout) {
 // Attention.  Rows are (new token, query head of the group) pairs; a
 // sequence of few rows runs in the rows kernel, of more in the tile kernel.
 // Both kernels decide from the sequence's own row count on the device, so a
-// batch may mix them.
+// batch may mix them.  Where the border lies: 16 sequences of 8192 keys, 32 on
+// 4 heads of 128, 8, 16 and 32 rows each in the rows kernel 30.7, 32.7 and
+// 50.6 us; 40, 64 and 128 rows in the tile kernel 75.2, 74.2 and 75.7.
 constexpr int kAttnFewRows = 32;          // most rows of a sequence in the rows kernel
 constexpr int kAttnRowsChunk = 128;       // keys: least share of a workgroup of the rows kernel
 constexpr int kAttnTileChunk = 256;       // ... of the tile kernel
@@ -149,12 +151,17 @@ inline bool make_plan_attention(int64_t T, int64_t B, int Hq, int Hkv, int D, in
     const int64_t G = Hq / Hkv, max_keys = max_pages * page;
     if (max_q > T) max_q = T;
     const int64_t most_rows = max_q * G;
+    // Three workgroups of the rows kernel a CU: four are resident, and the
+    // shares' remainders take the fourth's place (64 sequences of 2K to 16K
+    // keys, kernel and join together: target of 2 per CU 122 us, 3 112, 4 129,
+    // 6 118; one of 256K keys 59, 61, 64, 67).
     p->few_target = 3 * cu_count;
     p->tile_target = D == 64 ? 2 * cu_count : cu_count;
     auto ceil_div = [](int64_t a, int64_t b) { return (a + b - 1) / b; };
     // Where sequences have many rows on the average, the tile kernel takes the
     // few-row ones along: they run beside its tiles, the rows kernel would
-    // run before them.
+    // run before them (24 sequences, half of them decoding, half chunks of up
+    // to 700 tokens: 160 -> 145 us; one prompt: a launch less).
     if (most_rows <= kAttnFewRows || (G <= kAttnFewRows && T * G < 128 * B)) {
         p->few_tiles = (most_rows < kAttnFewRows ? most_rows : kAttnFewRows) > 16 ? 2 : 1;
         const int64_t units = B * Hkv;

@@ -6,9 +6,15 @@
 //                scale per token and head, written to their slots
 //   k_kv_read    the values that slots hold
 //
-// All three are bound by memory and by the launch.  A workgroup takes four
-// tokens (one wave each), or one token when there are few; a row (one head of
-// one token) lies across D / 8 lanes of a wave, eight values a lane.
+// A row (one head of one token) lies across D / 8 lanes of a wave, eight
+// values a lane.  All three are bound by memory where tokens are many (a copy
+// moves 5.12 TB/s here) and by the chain of dependent loads where they are few:
+//   rope of 8192 x 28 x 128 bf16   20.6 us for 117 MB (a copy of the same 17.7)
+//   write of 8192 x 4 x 128 bf16   11.8 us turned, 8.6 not (floor 4.9); of
+//                                  32768 tokens 32.6 and 24.1 (floor 19.6): the
+//                                  difference is the 64-bit angles and products
+//   read of 32768 x 4 x 128 bf16   19.4 us, its floor
+// back to back on the same tensors.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -227,6 +233,9 @@ __device__ __forceinline__ uint8_t *tile_of(const KvArgs &a, int slot, int h) {
     return a.cache + (((int64_t(page) * a.H + h) << sh) + in) * kv_tile_bytes(a.D);
 }
 
+// Heads of a workgroup of the sixteen-token form.  Four compute an angle for
+// more heads, two make more workgroups: 8192 tokens of 4 heads 11.6 and 11.8 us
+// turned, 9.6 and 8.6 not; 1024 tokens of 8 heads 8.4 and 6.6.
 constexpr int kWriteHeads = 2;
 
 // One token a workgroup.
@@ -278,7 +287,7 @@ __global__ __launch_bounds__(256) void k_kv_write(const TI *__restrict__ k, int6
 // Sixteen tokens of up to four heads a workgroup.  Codes pass through LDS so
 // that what is neighbours in the cache is written together: a key's 16 bytes
 // beside the next tokens', a value's four tokens as one dword (written a byte
-// at a time, 32768 tokens of 4 heads of 128 took 60 us).
+// at a time, 32768 tokens of 4 heads of 128 took 60 us; so 24).
 template <typename TI, Pairs P, int D>
 __global__ __launch_bounds__(256) void k_kv_write16(const TI *__restrict__ k, int64_t kdt, int64_t kdh,
                                                     const TI *__restrict__ v, int64_t vdt, int64_t vdh, RopeArgs r, KvArgs a,
@@ -420,8 +429,10 @@ __global__ __launch_bounds__(256) void k_kv_read(KvArgs a, TO *__restrict__ k, i
 }
 
 // ---------------------------------------------------------------------------
-// Launchers.  Four tokens a workgroup where that still gives every CU one.
+// Launchers.
 // ---------------------------------------------------------------------------
+// One token a workgroup of the rotation and of the read, until four of them
+// still give every CU four (rope of 1024 x 28 x 128: 4.7 us against 5.3).
 static bool few(int64_t T, int cu_count) { return T < 16 * int64_t(cu_count); }
 
 static Pairs pairs_of(int layout, int rot) { return layout && rot ? SIDE : rot / 2 % 4 == 0 ? ENDS : ODD; }
@@ -476,7 +487,8 @@ hipError_t launch_rope(int type, const void *x, int64_t ldt, int64_t ldh, int ou
 template <typename TI, Pairs P>
 static void write_laid(const TI *kk, int64_t kdt, int64_t kdh, const TI *vv, int64_t vdt, int64_t vdh, const RopeArgs &r,
                        const KvArgs &a, int64_t T, int cu_count, hipStream_t stream) {
-    // sixteen tokens a workgroup where every CU has one
+    // sixteen tokens a workgroup where every CU has one (1024 tokens of 8 heads of 128, turned: 8.4 -> 6.6 us), else one,
+    // whose chain of loads is shorter (64 tokens of 4 heads: 4.1 us)
     const unsigned groups = unsigned(a.H + kWriteHeads - 1) / kWriteHeads;
     if ((T + 15) / 16 * groups < int64_t(cu_count)) {
         k_kv_write<TI, P><<<dim3(unsigned(T)), 256, 0, stream>>>(kk, kdt, kdh, vv, vdt, vdh, r, a);
