@@ -450,3 +450,31 @@ def test_a_short_sequence_does_not_depend_on_its_neighbours_values():
     big = heads(500, 2, 128, F32, 77) * 100
     mmq.kv_write(big, big, a.cache, slots)
     assert torch.equal(a.run()[0], want[0])
+
+
+def test_two_calls_at_once():
+    """Two streams, each with its own batch and workspace, many times over: the results of either alone."""
+    a = Batch([1] * 6, [900, 3, 77, 2000, 16, 500], 28, 4, 128, 16, BF16, seed=21)
+    b = Batch([300, 1, 40], [700, 400, 1200], 8, 2, 64, 32, F16, seed=22)
+    want = [a.run(), b.run()]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    outs = []
+    for _ in range(10):
+        outs.append([x.run(stream=s) for x, s in zip((a, b), streams)])
+    torch.cuda.synchronize()
+    assert all(torch.equal(g, w) for got in outs for g, w in zip(got, want))
+
+
+def test_decode_step_by_step_equals_the_prompt():
+    """A prompt in one chunk and token by token: the same cache, rows within both calls' bounds of the exact ones."""
+    n = 90
+    whole = Batch([n], [n], 8, 2, 128, 16, BF16, seed=23)
+    check(whole, whole.run())
+    for i in (0, 1, 15, 16, 31, 32, 63, 64, 89):
+        one = torch.tensor([i + 1], dtype=torch.int32, device=DEV)
+        step = torch.tensor([0, 1], dtype=torch.int32, device=DEV)
+        got = mmq.attention_i8(whole.q[i:i + 1], whole.cache, whole.table, one, step)
+        want, bound = reference(whole, 128 ** -0.5)
+        off = (got[0].double() - want[i]).abs()
+        assert bool((off <= bound[i] * 1.01 + 2.0 ** -8 * want[i].abs() * 1.01).all())
