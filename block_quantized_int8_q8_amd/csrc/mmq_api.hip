@@ -790,6 +790,8 @@ int mmq_attention_i8(int type, const void *q, int64_t q_ldt, int64_t q_ldh, cons
     if (!q || !cache || !lens || !q_offsets || !out || (!page_table && max_pages > 0)) return refuse("null pointer argument");
     if (!aligned(q, 2) || !aligned(out, mmq::type_bytes(out_type))) return refuse("queries and output must be aligned to their type");
     if (!aligned(cache, 16)) return refuse("the cache must be 16-byte aligned");
+    if (q == out && (type != out_type || (T > 1 && q_ldt != out_ldt) || (q_heads > 1 && q_ldh != out_ldh)))
+        return refuse("attention: in place, type and strides of queries and output must be the same");
     if (!aligned(page_table, 4) || !aligned(lens, 4) || !aligned(q_offsets, 4))
         return refuse("page table, lengths and offsets must be 4-byte aligned");
     const int cus = gfx950_cus();

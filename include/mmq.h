@@ -502,7 +502,8 @@ int mmq_kv_read(int type, const void *cache, int64_t n_pages, int page, int head
  * p-w+1..p.  For each of its query heads h, with k_t and v_t the values that
  * the cache holds for head h / (q_heads / kv_heads),
  *   out = sum_t softmax_t(scale * q . k_t) v_t.
- *   q: [T, q_heads, D], bf16 or fp16; out: the same shape, of q's type or fp32;
+ *   q: [T, q_heads, D], bf16 or fp16; out: the same shape, of q's type or fp32,
+ *   may be q itself (same type and strides), else must not overlap the inputs;
  *   page_table: int32 [n_seqs][max_pages]; lens: int32 [n_seqs]; q_offsets:
  *   int32 [n_seqs + 1], not decreasing.
  *   max_q: the most new tokens of a sequence; a sequence with more has only

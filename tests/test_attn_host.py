@@ -37,7 +37,7 @@ def read(type=0, cache=OK, n_pages=8, page=16, H=8, D=64, slots=OK, T=4, k=OK, k
 
 
 def attention(type=1, q=OK, qdt=512, qdh=64, cache=OK, n_pages=8, page=16, table=OK, max_pages=4, lens=OK, offsets=OK, B=2, T=4,
-              max_q=4, Hq=8, Hkv=2, D=64, scale=0.1, window=0, out_type=1, out=OK, odt=512, odh=64, ws=OK, wn=1 << 40):
+              max_q=4, Hq=8, Hkv=2, D=64, scale=0.1, window=0, out_type=1, out=2 * OK, odt=512, odh=64, ws=OK, wn=1 << 40):
     return mmq.lib().mmq_attention_i8(type, p(q), qdt, qdh, p(cache), n_pages, page, p(table), max_pages, p(lens), p(offsets), B, T,
                                       max_q, Hq, Hkv, D, scale, window, out_type, p(out), odt, odh, p(ws), wn, None)
 
@@ -77,7 +77,8 @@ CALLS = {
         (dict(odt=500), "overlap"), (dict(scale=nan), "scale"), (dict(scale=math.inf), "scale"), (dict(window=-1), "window"),
         (dict(q=None), "null"), (dict(cache=None), "null"), (dict(table=None), "null"), (dict(lens=None), "null"),
         (dict(offsets=None), "null"), (dict(out=None), "null"), (dict(q=OK + 1), "aligned"), (dict(out_type=0, out=OK + 2), "aligned"),
-        (dict(cache=OK + 8), "aligned"), (dict(lens=OK + 2), "aligned"), (dict(table=OK + 1), "aligned"), (dict(offsets=OK + 3), "aligned")]),
+        (dict(cache=OK + 8), "aligned"), (dict(lens=OK + 2), "aligned"), (dict(table=OK + 1), "aligned"), (dict(offsets=OK + 3), "aligned"),
+        (dict(out=OK, out_type=0), "in place"), (dict(out=OK, odt=1024), "in place"), (dict(out=OK, odh=64, odt=640), "in place")]),
 }
 REFUSALS = [(n, kw, why) for n, (_, cases) in CALLS.items() for kw, why in cases]
 

@@ -478,3 +478,12 @@ def test_decode_step_by_step_equals_the_prompt():
         want, bound = reference(whole, 128 ** -0.5)
         off = (got[0].double() - want[i]).abs()
         assert bool((off <= bound[i] * 1.01 + 2.0 ** -8 * want[i].abs() * 1.01).all())
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("new,lens", [([1] * 5, [900, 3, 77, 2000, 16]), ([300, 1], [700, 400]), ([4, 70], [3000, 70]), ([2500], [2500])])
+def test_output_over_the_queries(new, lens, D):
+    bt = Batch(new, lens, 16, 4, D, 16, F16, seed=24)
+    want = bt.run()
+    assert bt.run(out=bt.q) is bt.q
+    assert torch.equal(bt.q, want)
