@@ -912,9 +912,10 @@ __global__ __launch_bounds__(256) void k_attn_join_tiles(AttnArgs a) {
     const int64_t slot0 = int64_t(unit) * a.split * BM + slot_r;
     const float *ml = a.part + int64_t(a.units) * a.Hkv * a.split * BM * D;
     float to = -__builtin_inff();
+#pragma unroll 8
     for (int k = 0; k < shares; k++) to = fmaxf(to, ml[2 * (slot0 + int64_t(k) * BM)]);
     Joined j{{0, 0, 0, 0}, 0.0f};
-#pragma unroll 4
+#pragma unroll 8
     for (int k = 0; k < shares; k++) {
         const int64_t slot = slot0 + int64_t(k) * BM;
         j.add(ml[2 * slot], ml[2 * slot + 1], *reinterpret_cast<const f32x4 *>(a.part + slot * D + d), to);

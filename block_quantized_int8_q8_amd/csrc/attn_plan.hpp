@@ -114,8 +114,8 @@ inline const char *check_rope(int D, int rot, int layout) {
 // sequence of few rows runs in the rows kernel, of more in the tile kernel.
 // Both kernels decide from the sequence's own row count on the device, so a
 // batch may mix them.  Where the border lies: 16 sequences of 8192 keys, 32 on
-// 4 heads of 128, 8, 16 and 32 rows each in the rows kernel 30.7, 32.7 and
-// 50.6 us; 40, 64 and 128 rows in the tile kernel 75.2, 74.2 and 75.7.
+// 4 heads of 128, 8, 16 and 32 rows each in the rows kernel 30, 32 and 49 us;
+// 40, 64 and 128 rows in the tile kernel 71, 70 and 76.
 constexpr int kAttnFewRows = 32;          // most rows of a sequence in the rows kernel
 constexpr int kAttnRowsChunk = 128;       // keys: least share of a workgroup of the rows kernel
 constexpr int kAttnTileChunk = 256;       // ... of the tile kernel
@@ -162,7 +162,9 @@ inline bool make_plan_attention(int64_t T, int64_t B, int Hq, int Hkv, int D, in
     // few-row ones along: they run beside its tiles, the rows kernel would
     // run before them (24 sequences, half of them decoding, half chunks of up
     // to 700 tokens: 160 -> 145 us; one prompt: a launch less).
-    if (most_rows <= kAttnFewRows || (G <= kAttnFewRows && T * G < 128 * B)) {
+    // And where T says that all have max_q, none has few (16 sequences of 40
+    // rows over 8192 keys 75 -> 71 us).
+    if (most_rows <= kAttnFewRows || (G <= kAttnFewRows && T * G < 128 * B && T < B * max_q)) {
         p->few_tiles = (most_rows < kAttnFewRows ? most_rows : kAttnFewRows) > 16 ? 2 : 1;
         const int64_t units = B * Hkv;
         int64_t s = ceil_div(4 * int64_t(p->few_target), units);        // lengths differ: more shares than the device needs
