@@ -487,3 +487,14 @@ def test_output_over_the_queries(new, lens, D):
     want = bt.run()
     assert bt.run(out=bt.q) is bt.q
     assert torch.equal(bt.q, want)
+
+
+@pytest.mark.parametrize("Hq", [4, 40])
+@pytest.mark.parametrize("offsets", [[0, 5, 2, 8], [3, 3, -7, 9], [9, 4, 1, 0], [-100, 2 ** 31 - 1, 0, 5]])
+def test_offsets_that_decrease_stay_within_the_rows(offsets, Hq):
+    """What rows between decreasing offsets hold is not said; rows past the last offset anyone names are left."""
+    bt = Batch([3, 3, 3], [100, 40, 300], Hq, 1, 64, 16, F16, behind=0)
+    store = torch.full((20, Hq, 64), 3.0, dtype=F16, device=DEV)
+    mmq.attention_i8(bt.q, bt.cache, bt.table, bt.lens, torch.tensor(offsets, dtype=torch.int32, device=DEV), out=store[5:14])
+    assert bool((store[:5] == 3.0).all()) and bool((store[14:] == 3.0).all())
+    assert bool(store.isfinite().all())
