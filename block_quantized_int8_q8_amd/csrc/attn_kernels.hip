@@ -526,11 +526,16 @@ __global__ __launch_bounds__(64 * WAVES) void k_attn_tile(AttnArgs a) {
     const int r = row0 + 32 * wv + col, tok = r / a.G;
     const bool there = r < rows;
     const int pos = there ? s.pos0 + tok : -1, first = a.window ? pos - a.window : -1;
+    // A lane past the last row has zeros: any row that it could read instead is one that, with the output over the
+    // queries, another workgroup may be writing.
     x8 q[KS];
-    {
-        const T *qr = static_cast<const T *>(a.q) + int64_t(s.start + (there ? tok : 0)) * a.qdt + int64_t(h * a.G + (there ? r - tok * a.G : 0)) * a.qdh;
+    if (there) {
+        const T *qr = static_cast<const T *>(a.q) + int64_t(s.start + tok) * a.qdt + int64_t(h * a.G + r - tok * a.G) * a.qdh;
 #pragma unroll
         for (int k = 0; k < KS; k++) q[k] = load_x8(qr + 16 * k + 8 * hf);
+    } else {
+#pragma unroll
+        for (int k = 0; k < KS; k++) q[k] = x8{};
     }
     // the wave's rows see all of keys (lo_all, hi_all], and something in steps [from, to]
     const int wr0 = row0 + 32 * wv, wr1 = min(wr0 + 32, rows) - 1;
@@ -539,7 +544,7 @@ __global__ __launch_bounds__(64 * WAVES) void k_attn_tile(AttnArgs a) {
     const bool active = wr0 < rows && hi_any >= begin && lo_any < end;
     const int from = active ? max(lo_any + 1 - begin, 0) / 64 : steps, to = active ? min((hi_any - begin) / 64, steps - 1) : -1;
 
-    float m = NEG, l = 0.0f;
+    float m = there ? NEG : -NEG, l = 0.0f;               // infinity: a lane without a row never asks for another reference
     f32x16 o[DT];
 #pragma unroll
     for (int d = 0; d < DT; d++)
