@@ -176,8 +176,8 @@ __device__ __forceinline__ int few_chunk(const AttnArgs &a) {
 // Softmax of the transposed scores in a lane's registers.
 //
 // Scores t are in units of log2, p = 2^(t - m) for a running reference m of
-// the row, which moves up only, and only when a new maximum lies more than
-// 2^8 above.  The second product's operand is p * dv in 16 bits.  In fp16 its
+// the row, which moves up only, and only when that row has a new maximum more
+// than 2^8 above.  The second product's operand is p * dv in 16 bits.  In fp16 its
 // exponents end at 15 and -24, so there m must follow t + log2 dv: the largest
 // p * dv lies between 2^6 and 2^14, whatever the size of dv.
 //   Tile kernel: the scale goes into the exponent, p' = 2^(t + log2 dv - m) =
@@ -319,9 +319,10 @@ __global__ __launch_bounds__(256) void k_attn_rows(AttnArgs a) {
             float want = Half<T>::NARROW ? fmaxf(low - kTop, top - kNarrowSum) : top;
             want = fmaxf(want, __shfl_xor(want, 16));
             want = fmaxf(want, __shfl_xor(want, 32));
-            if (__any(want > m[rb] + kSlack || (m[rb] == NEG && want > NEG))) {
-                const float to = fmaxf(m[rb], want), f = to == NEG ? 1.0f : __builtin_amdgcn_exp2f(m[rb] - to);
-                m[rb] = to;
+            const bool up = want > m[rb] + kSlack || (m[rb] == NEG && want > NEG);
+            if (__any(up)) {                                          // rows that do not need it stay where they are
+                const float f = up ? __builtin_amdgcn_exp2f(m[rb] - want) : 1.0f;
+                m[rb] = up ? want : m[rb];
                 l[rb] *= f;
 #pragma unroll
                 for (int c = 0; c < C; c++)
@@ -696,9 +697,10 @@ __global__ __launch_bounds__(64 * WAVES) void k_attn_tile(AttnArgs a) {
                 top = max_of_halves(top);
             }
             const float want = top - kTop;
-            if (__any(want > m + kSlack || (m == NEG && want > NEG))) {
-                const float up = fmaxf(m, want), f = up == NEG ? 1.0f : __builtin_amdgcn_exp2f(m - up);
-                m = up;
+            const bool up = want > m + kSlack || (m == NEG && want > NEG);
+            if (__any(up)) {                              // rows that do not need it stay where they are
+                const float f = up ? __builtin_amdgcn_exp2f(m - want) : 1.0f;
+                m = up ? want : m;
                 l *= f;
 #pragma unroll
                 for (int d = 0; d < DT; d++)
