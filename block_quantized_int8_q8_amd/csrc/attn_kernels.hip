@@ -62,7 +62,6 @@ struct AttnArgs {
 template <typename T> struct Half;
 template <> struct Half<__bf16> {
     typedef bf16x8 x8;
-    static constexpr bool NARROW = false;
     static __device__ __forceinline__ f32x4 mfma16(x8 a, x8 b, f32x4 c) { return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0); }
     static __device__ __forceinline__ f32x16 mfma32(x8 a, x8 b, f32x16 c) { return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0); }
     // Four int8 codes as two dwords.  Integers below 256 have zeros in the low half of their fp32 form.
@@ -75,7 +74,6 @@ template <> struct Half<__bf16> {
 };
 template <> struct Half<_Float16> {
     typedef f16x8 x8;
-    static constexpr bool NARROW = true;         // exponents from -24 to 15 only
     static __device__ __forceinline__ f32x4 mfma16(x8 a, x8 b, f32x4 c) { return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0); }
     static __device__ __forceinline__ f32x16 mfma32(x8 a, x8 b, f32x16 c) { return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0); }
     // code + 128 as the low bits of 1024 + code + 128, less 1152: exact.
@@ -175,21 +173,52 @@ __device__ __forceinline__ int few_chunk(const AttnArgs &a) {
 // ---------------------------------------------------------------------------
 // Softmax of the transposed scores in a lane's registers.
 //
-// Scores t are in units of log2, p = 2^(t - m) for a running reference m of
-// the row, which moves up only, and only when that row has a new maximum more
-// than 2^8 above.  The second product's operand is p * dv in 16 bits.  In fp16 its
-// exponents end at 15 and -24, so there m must follow t + log2 dv: the largest
-// p * dv lies between 2^6 and 2^14, whatever the size of dv.
-//   Tile kernel: the scale goes into the exponent, p' = 2^(t + log2 dv - m) =
-// p * dv, one FMA on the product where two multiplications were (the sum of
-// p takes p' / dv), and m = max(t + log2 dv) - 6 for both types.
-//   Rows kernel, a few scores a lane: p and p * dv are formed apart.  In bf16
-// m = max(t); in fp16 (NARROW) m = max(t + log2 dv) - 6, but not so low that
-// the sum of p leaves fp32 (m >= max(t) - 60: where that binds, the output is
-// below 2^-47).
+// Scores t are in units of log2.  The second product's operand is a weight
+// times its value's scale dv in 16 bits, and that scale goes into the exponent:
+//   p' = 2^(t + log2 dv - m) = p dv,   the sum of the weights takes p' / dv,
+// one FMA on the product where two multiplications were.  m is a running
+// reference of the row, which moves up only, and only when that row has a new
+// maximum of t + log2 dv more than 2^8 above the last: the largest p' lies
+// between 2^6 and 2^14, within fp16's exponents (-24 to 15) whatever the size
+// of dv.
+//   A p' below 2^-126 is lost from the sum of the weights too, so a value's
+// scale counts as some least one: 2^-100, or 2^-108 of the largest so far where
+// that is above 2^8 (values past 32000; in the rows kernel, of the largest that
+// the row sees and that moved its reference, and in the tile kernel of all that
+// its workgroup has read).  So keys, those of zeros among them, keep their
+// weight beside values of any size: none above 2^-23 of the row's largest is
+// lost.
+//   The sum may stand far from the reference, from 2^-115 (one value, the
+// largest there is) to 2^139 (2^25 values of next to nothing): it is held in
+// units of 2^12, so that neither end leaves fp32 (values past 2^121 leave its
+// terms 16 bits), and where the reference moves it is scaled in two halves,
+// since 2^(m - m') may be below 2^-126 where the sum times it is not.
 // ---------------------------------------------------------------------------
 constexpr float kSlack = 8.0f;
-constexpr float kTop = 6.0f, kNarrowSum = 60.0f;
+constexpr float kTop = 6.0f;
+constexpr float kLeastScale = 0x1p-100f, kLargeScale = 0x1p8f, kScaleRange = 0x1p-108f;
+constexpr float kSumUnit = 0x1p12f;
+
+// The least scale, raised by a wave's scales of which some are large.
+__device__ __forceinline__ float raised_least(float least, float scale) {
+    scale = scale == scale ? scale : 0.0f;
+#pragma unroll
+    for (int o = 32; o; o >>= 1) scale = fmaxf(scale, __shfl_xor(scale, o));
+    return fmaxf(least, scale * kScaleRange);
+}
+
+// 2^x times a sum, whatever the size of 2^x alone.
+__device__ __forceinline__ float scaled_sum(float l, float x) {
+    const float h = __builtin_amdgcn_exp2f(0.5f * x);
+    return l * h * h;
+}
+// Outputs over their sum of weights (in its units; 0: the row saw nothing).
+// Neither end of the sum's range has a reciprocal in fp32 as it is.
+__device__ __forceinline__ f32x4 over_sum(f32x4 o, float l) {
+    if (l == 0.0f) return f32x4{0, 0, 0, 0};
+    const bool low = l < 1.0f;
+    return o * (1.0f / (low ? l * 0x1p32f : l)) * (low ? 0x1p32f / kSumUnit : 1.0f / kSumUnit);
+}
 
 // The larger of the values of lanes i and i + 32, in both.
 __device__ __forceinline__ float max_of_halves(float x) {
@@ -234,26 +263,27 @@ __global__ __launch_bounds__(256) void k_attn_rows(AttnArgs a) {
     const bool two = RT > 1 && rows > 16;
 
     // this lane's rows: one of each block of 16
-    int pos[RT], first[RT];
+    int pos[RT];
+    const uint32_t span = a.window ? uint32_t(a.window) : 0x80000000u;      // keys that a row sees, up to its position
     x8 q[RT][2 * C];
 #pragma unroll
     for (int rb = 0; rb < RT; rb++) {
         const int r = 16 * rb + col, i = r / a.G;
         const bool there = r < rows;
         pos[rb] = there ? s.pos0 + i : -1;
-        first[rb] = a.window ? pos[rb] - a.window : -1;              // keys after this one
         const T *qr = static_cast<const T *>(a.q) + int64_t(s.start + (there ? i : 0)) * a.qdt + int64_t(h * a.G + (there ? r - i * a.G : 0)) * a.qdh;
 #pragma unroll
         for (int c = 0; c < C; c++)
 #pragma unroll
             for (int e = 0; e < 2; e++) q[rb][2 * c + e] = load_x8(qr + 64 * c + 16 * g + 8 * e);
     }
-    float m[RT], l[RT];
+    float m[RT], l[RT], least[RT];
     f32x4 o[RT][C][4];
 #pragma unroll
     for (int rb = 0; rb < RT; rb++) {
         m[rb] = NEG;
         l[rb] = 0.0f;
+        least[rb] = kLeastScale;
 #pragma unroll
         for (int c = 0; c < C; c++)
 #pragma unroll
@@ -300,30 +330,57 @@ __global__ __launch_bounds__(256) void k_attn_rows(AttnArgs a) {
                         if (rb == 0 || two) sc[rb][j] = Half<T>::mfma16(k, q[rb][2 * c + e], sc[rb][j]);
                 }
         }
+#pragma unroll
+        for (int j = 0; j < 2; j++)
+#pragma unroll
+            for (int i = 0; i < 4; i++) ks[j][i] = __builtin_fmaf(ks[j][i], a.scale, vs[j][i] - vs[j][i]);      // a value's NaN with the key's scale
         x8 p8[RT];
 #pragma unroll
         for (int rb = 0; rb < RT; rb++) {
             if (rb > 0 && !two) continue;
-            float t[2][4], top = NEG, low = NEG;
-            bool seen[2][4];
+            float t[2][4], counted[2][4];
+            auto of_row = [](float x) {                              // the largest of a row's four lanes
+                x = fmaxf(x, __shfl_xor(x, 16));
+                return fmaxf(x, __shfl_xor(x, 32));
+            };
+            auto wanted = [&] {                                      // the reference that would suit these scores
+                float top = NEG;
+#pragma unroll
+                for (int e = 0; e < 8; e++) top = fmaxf(top, t[e / 4][e % 4]);
+                return of_row(top) - kTop;
+            };
 #pragma unroll
             for (int j = 0; j < 2; j++)
 #pragma unroll
                 for (int i = 0; i < 4; i++) {
                     const int key = key0 + 16 * j + 4 * g + i;
-                    seen[j][i] = there[j] && key <= pos[rb] && key > first[rb];
-                    t[j][i] = seen[j][i] ? sc[rb][j][i] * (ks[j][i] * a.scale) : NEG;
-                    top = fmaxf(top, t[j][i]);
-                    if (Half<T>::NARROW) low = fmaxf(low, seen[j][i] ? t[j][i] + __builtin_amdgcn_logf(vs[j][i]) : NEG);
+                    const bool seen = there[j] && uint32_t(pos[rb] - key) < span;
+                    counted[j][i] = fmaxf(vs[j][i], least[rb]);
+                    t[j][i] = seen ? __builtin_fmaf(sc[rb][j][i], ks[j][i], __builtin_amdgcn_logf(counted[j][i])) : NEG;
                 }
-            float want = Half<T>::NARROW ? fmaxf(low - kTop, top - kNarrowSum) : top;
-            want = fmaxf(want, __shfl_xor(want, 16));
-            want = fmaxf(want, __shfl_xor(want, 32));
+            float want = wanted();
             const bool up = want > m[rb] + kSlack || (m[rb] == NEG && want > NEG);
             if (__any(up)) {                                          // rows that do not need it stay where they are
+                float large = 0.0f;
+#pragma unroll
+                for (int e = 0; e < 8; e++) large = fmaxf(large, t[e / 4][e % 4] > NEG ? counted[e / 4][e % 4] : 0.0f);
+                large = of_row(large) * kScaleRange;
+                large = up ? fmaxf(large, least[rb]) : least[rb];
+                if (__any(large > least[rb])) {
+#pragma unroll
+                    for (int j = 0; j < 2; j++)
+#pragma unroll
+                        for (int i = 0; i < 4; i++) {
+                            const float more = fmaxf(counted[j][i], large);
+                            if (t[j][i] > NEG) t[j][i] += __builtin_amdgcn_logf(more) - __builtin_amdgcn_logf(counted[j][i]);
+                            counted[j][i] = more;
+                        }
+                    least[rb] = large;
+                    want = wanted();
+                }
                 const float f = up ? __builtin_amdgcn_exp2f(m[rb] - want) : 1.0f;
+                l[rb] = up ? scaled_sum(l[rb], m[rb] - want) : l[rb];
                 m[rb] = up ? want : m[rb];
-                l[rb] *= f;
 #pragma unroll
                 for (int c = 0; c < C; c++)
 #pragma unroll
@@ -336,8 +393,8 @@ __global__ __launch_bounds__(256) void k_attn_rows(AttnArgs a) {
 #pragma unroll
                 for (int i = 0; i < 4; i++) {
                     const float p = __builtin_amdgcn_exp2f(t[j][i] - ref);
-                    l[rb] += p;
-                    w[4 * j + i] = T(seen[j][i] ? p * vs[j][i] : 0.0f);
+                    l[rb] = __builtin_fmaf(p, __builtin_amdgcn_rcpf(counted[j][i]) * (1.0f / kSumUnit), l[rb]);
+                    w[4 * j + i] = T(p);
                 }
             __builtin_memcpy(&p8[rb], w, 16);
         }
@@ -393,11 +450,11 @@ __global__ __launch_bounds__(256) void k_attn_rows(AttnArgs a) {
                 to = fmaxf(to, S_m[w][r]);
             }
 #pragma unroll
-            for (int w = 0; w < 4; w++) sum += S_m[w][r] == NEG ? S_l[w][r] : S_l[w][r] * __builtin_amdgcn_exp2f(S_m[w][r] - to);
+            for (int w = 0; w < 4; w++) sum += S_m[w][r] == NEG ? S_l[w][r] : scaled_sum(S_l[w][r], S_m[w][r] - to);
             if (alone) {
                 const int i = r / a.G;
                 O *out = static_cast<O *>(a.out) + int64_t(s.start + i) * a.odt + int64_t(h * a.G + r - i * a.G) * a.odh;
-                store4(out + 64 * c + d, sum == 0.0f ? f32x4{0, 0, 0, 0} : v * (1.0f / sum));
+                store4(out + 64 * c + d, over_sum(v, sum));
             } else {
                 const int64_t slot = ((int64_t(b) * a.Hkv + h) * a.split + share) * R + r;
                 *reinterpret_cast<f32x4 *>(a.part + slot * D + 64 * c + d) = v;
@@ -558,7 +615,7 @@ __global__ __launch_bounds__(64 * WAVES) void k_attn_tile(AttnArgs a) {
         u32x4 st[LOADS];
         float scale;                                      // wave 0: of a key; wave 1: of a value
     };
-    float last_scale = 1.0f;
+    float least = kLeastScale;
     int tk = -1, tv = -1;                                 // cache tiles of 16 steps: lane 4 i + j holds 16-key tile j of step i
     int valid = 0;                                        // four bits a step, of four steps: which of its tiles are there
     auto load = [&](int step, Stage &g) __attribute__((always_inline)) {
@@ -610,16 +667,10 @@ __global__ __launch_bounds__(64 * WAVES) void k_attn_tile(AttnArgs a) {
     auto store_scales = [&](const Stage &g, int step) __attribute__((always_inline)) {
         if (wv == 0) S_ks[step & 3][lane] = g.scale * a.scale;
         if (wv == 1) {
-            // A row of zeros has scale 0.  Any other does for its codes: 2^-40
-            // of its lane's last, 1 at most, which keeps its weight for the
-            // sum and leaves the reference to the rows that are not zero.
-            // Below 2^-100 the exponential would lose the row's weight with
-            // its value: there a scale counts as 2^-100.
-            const float stand_in = fmaxf(last_scale * 0x1p-40f, 0x1p-100f);
-            const float sc = g.scale >= 0x1p-100f || g.scale != g.scale ? g.scale : g.scale == 0.0f ? stand_in : 0x1p-100f;
-            if (g.scale >= 0x1p-100f) last_scale = fminf(g.scale, 1.0f);
-            S_lv[step & 3][lane] = __builtin_amdgcn_logf(sc);
-            S_rv[step & 3][lane] = sc == sc ? __builtin_amdgcn_rcpf(sc) : 1.0f;       // NaN reaches a row by the logarithm, if it is seen
+            if (__any(g.scale > kLargeScale)) least = raised_least(least, g.scale);
+            const float sc = fmaxf(g.scale, least);
+            S_lv[step & 3][lane] = g.scale == g.scale ? __builtin_amdgcn_logf(sc) : g.scale;      // NaN reaches its rows by this, if it is seen
+            S_rv[step & 3][lane] = __builtin_amdgcn_rcpf(sc) * (1.0f / kSumUnit);
         }
     };
     auto store_all = [&](const Stage &g, int step, int kslot, int vslot) __attribute__((always_inline)) {
@@ -665,7 +716,7 @@ __global__ __launch_bounds__(64 * WAVES) void k_attn_tile(AttnArgs a) {
     constexpr int AHEAD = 4;
     float top = NEG;
     x8 fr[AHEAD];
-    f32x4 r4[2];                                          // reciprocals of the values' scales, two fours ahead
+    f32x4 r4[2];                                          // reciprocals of the values' scales (and the sum's unit), two fours ahead
     int ring = 0;                                         // of this step's keys and values; the next step's is behind it
     auto next = [](int x) { return x + 1 == RING ? 0 : x + 1; };
     auto prefetch_r = [&](int step) __attribute__((always_inline)) {
@@ -700,8 +751,8 @@ __global__ __launch_bounds__(64 * WAVES) void k_attn_tile(AttnArgs a) {
             const bool up = want > m + kSlack || (m == NEG && want > NEG);
             if (__any(up)) {                              // rows that do not need it stay where they are
                 const float f = up ? __builtin_amdgcn_exp2f(m - want) : 1.0f;
+                l = up ? scaled_sum(l, m - want) : l;
                 m = up ? want : m;
-                l *= f;
 #pragma unroll
                 for (int d = 0; d < DT; d++)
 #pragma unroll
@@ -806,7 +857,6 @@ __global__ __launch_bounds__(64 * WAVES) void k_attn_tile(AttnArgs a) {
     l += __shfl_xor(l, 32);
     if (!there) return;
     // register i of o[2 v + p]: column 64 v + 32 (i / 4 % 2) + 16 hf + 4 (i % 4) + 2 p + i / 8
-    const float inv = alone ? (l == 0.0f ? 0.0f : 1.0f / l) : 1.0f;
     const int64_t slot = ((int64_t(rest % a.units) * a.Hkv + h) * a.split + share) * BM + 32 * wv + col;
     O *out = static_cast<O *>(a.out) + int64_t(s.start + tok) * a.odt + int64_t(h * a.G + r - tok * a.G) * a.odh;
 #pragma unroll
@@ -816,9 +866,9 @@ __global__ __launch_bounds__(64 * WAVES) void k_attn_tile(AttnArgs a) {
 #pragma unroll
             for (int y = 0; y < 4; y++) {
                 const int i = 4 * x + y, d = 64 * v + 32 * x + 16 * hf + 4 * y;
-                const f32x4 w = {o[2 * v][i] * inv, o[2 * v][i + 8] * inv, o[2 * v + 1][i] * inv, o[2 * v + 1][i + 8] * inv};
+                const f32x4 w = {o[2 * v][i], o[2 * v][i + 8], o[2 * v + 1][i], o[2 * v + 1][i + 8]};
                 if (alone)
-                    store4(out + d, l == 0.0f ? f32x4{0, 0, 0, 0} : w);
+                    store4(out + d, over_sum(w, l));
                 else
                     *reinterpret_cast<f32x4 *>(a.part + slot * D + d) = w;
             }
@@ -838,15 +888,15 @@ struct Joined {
     // One share, for the largest reference `to` of all: one that saw no
     // finite maximum adds nothing, unless it holds a NaN.
     __device__ __forceinline__ void add(float m, float l, f32x4 o, float to) {
-        const float f = m == -__builtin_inff() ? 0.0f : __builtin_amdgcn_exp2f(m - to);
-        sum += m == -__builtin_inff() ? l : l * f;
-        v += o * f;
+        const bool none = m == -__builtin_inff();
+        sum += none ? l : scaled_sum(l, m - to);
+        v += o * (none ? 0.0f : __builtin_amdgcn_exp2f(m - to));
     }
     template <typename O>
     __device__ __forceinline__ void write(const AttnArgs &a, const Seq &s, int h, int r, int d) const {
         const int i = r / a.G;
         O *out = static_cast<O *>(a.out) + int64_t(s.start + i) * a.odt + int64_t(h * a.G + r - i * a.G) * a.odh;
-        store4(out + d, sum == 0.0f ? f32x4{0, 0, 0, 0} : v * (1.0f / sum));
+        store4(out + d, over_sum(v, sum));
     }
 };
 

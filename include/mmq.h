@@ -510,15 +510,19 @@ int mmq_kv_read(int type, const void *cache, int64_t n_pages, int page, int head
  *   its first max_q computed.
  * Rounding: q and the codes enter the products as they are, sums are fp32;
  * exp(..) times a value's scale is rounded to q's type for the second
- * product, and the output once to its own.  Weights below 2^-118 of a row's
- * largest may be lost, and a value's scale below 2^-100 may count as 2^-100.
+ * product, and the output once to its own.  A value's scale below 2^-100, or
+ * below 2^-108 of the largest of its sequence, may count as that.  Where a
+ * key's weight times its value's scale (as it counts) is below 2^-118 of its
+ * row's largest such product, its part of the output may be lost, and below
+ * 2^-131 its part of the sum of the weights: of no weight above 2^-23 of its
+ * row's largest.
  * A row that sees no key (lens 0, or fewer tokens than new ones) gets zeros.
  * Keys on a page whose number is outside 0..n_pages-1 are not seen.  A seen
  * key or value with scale NaN makes its rows NaN; what is not seen has no
- * effect, whatever it holds.  Rows of out outside every sequence, and past
- * max_q, are left as they were.  Lengths are clamped to 0..max_pages*page and
- * offsets to 0..T; where offsets decrease, rows between them are unspecified,
- * but nothing outside the buffers is read or written.
+ * effect (but for that largest scale), whatever it holds.  Rows of out outside
+ * every sequence, and past max_q, are left as they were.  Lengths are clamped to
+ * 0..max_pages*page and offsets to 0..T; where offsets decrease, rows between
+ * them are unspecified, but nothing outside the buffers is read or written.
  * T * q_heads <= 2^30; n_seqs <= 2^20; max_pages * page <= 2^30; a grid of
  * more than 2^22 workgroups (n_seqs * kv_heads and more) is refused.
  * The same bits on every run; which shares a sequence's keys are split into

@@ -25,7 +25,8 @@ def test_output_over_the_queries_whenever_its_workgroups_run(new, lens, Hq, Hkv,
 
 @pytest.mark.parametrize("t", [BF16, F16])
 @pytest.mark.parametrize("new,lens,Hq,Hkv,D", [([1], [3000], 8, 1, 128), ([1] * 220, [400] * 220, 28, 4, 64),
-                                               ([3, 1], [900, 2500], 8, 1, 64), ([1], [700], 32, 1, 256), ([150], [900], 4, 1, 128), ([200], [200], 8, 2, 64), ([90], [700], 4, 1, 256)])
+                                               ([3, 1], [900, 2500], 8, 1, 64), ([1], [700], 32, 1, 256),
+                                               ([150], [900], 4, 1, 128), ([200], [200], 8, 2, 64), ([90], [700], 4, 1, 256)])
 def test_a_row_does_not_depend_on_the_other_rows_queries(new, lens, Hq, Hkv, D, t):
     """Rows of a wave share its products, and one whose scores rise makes the wave rescale: every third row's query is
     made forty times as large, and the others keep their bits."""
