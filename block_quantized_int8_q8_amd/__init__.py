@@ -805,7 +805,7 @@ def attention_i8(q, cache, page_table, lens, q_offsets, max_q=None, scale=None, 
                  workspace=None, stream=None):
     """Attention of new tokens ([T, query heads, D] bf16/fp16) over the cache
     that already holds them -> [T, query heads, D] of ``dtype`` (q's, or
-    float32).  Sequence b: ``lens[b]`` tokens on the pages ``page_table[b]``,
+    float32, which has softmax weights of more bits too).  Sequence b: ``lens[b]`` tokens on the pages ``page_table[b]``,
     the last ``q_offsets[b + 1] - q_offsets[b]`` of them new, rows q_offsets[b]..
     of q; all int32, on the GPU.  ``max_q``: the most new tokens of a sequence
     (T by default; 1 while decoding saves a launch); ``scale``: 1 / sqrt(D) by

@@ -14,9 +14,17 @@
 // over the keys t that the row may see.  Codes are at most 127 in magnitude
 // and so exact in 16 bits: the two products run on the 16-bit matrix core
 // with q and the codes as they are, both scales are applied in fp32, and the
-// one rounding between q and the result is that of exp(s_t) dv_t to 16 bits
-// (the type of q), which the second product reads.  Sums, maxima and the
-// running output are fp32.
+// one rounding between q and the result is that of exp(s_t) dv_t, which the
+// second product reads in 16 bits (the type of q).  Sums, maxima and the running
+// output are fp32.
+//   The weights' bits are chosen by what they cost.  Where the output is fp32,
+// and in the rows kernel always, what the rounding leaves is rounded too and
+// multiplied by a second product (16 bits in bf16, 22 in fp16): fp32 outputs
+// would have no use for theirs otherwise, and the rows kernel waits for memory
+// (64 sequences 109 -> 110.5 us; the mean error against 64 bits falls from
+// 0.0022 to 0.0014 of the mean magnitude, what the output's own rounding
+// leaves).  In the tile kernel it takes the 8K prompt from 535 to 707 us, so
+// there a 16-bit output has weights of as many bits as itself (0.0022).
 //
 // Both products are formed transposed, keys (or value columns) by rows, so
 // that a lane holds scores of one row only: the maximum and the sum of a
@@ -334,7 +342,7 @@ __global__ __launch_bounds__(256) void k_attn_rows(AttnArgs a) {
         for (int j = 0; j < 2; j++)
 #pragma unroll
             for (int i = 0; i < 4; i++) ks[j][i] = __builtin_fmaf(ks[j][i], a.scale, vs[j][i] - vs[j][i]);      // a value's NaN with the key's scale
-        x8 p8[RT];
+        x8 p8[RT], rest8[RT];                                        // weights, and what their rounding leaves
 #pragma unroll
         for (int rb = 0; rb < RT; rb++) {
             if (rb > 0 && !two) continue;
@@ -387,7 +395,7 @@ __global__ __launch_bounds__(256) void k_attn_rows(AttnArgs a) {
                     for (int k = 0; k < 4; k++) o[rb][c][k] *= f;
             }
             const float ref = m[rb] == NEG ? 0.0f : m[rb];
-            T w[8];
+            T w[8], rest[8];
 #pragma unroll
             for (int j = 0; j < 2; j++)
 #pragma unroll
@@ -395,8 +403,10 @@ __global__ __launch_bounds__(256) void k_attn_rows(AttnArgs a) {
                     const float p = __builtin_amdgcn_exp2f(t[j][i] - ref);
                     l[rb] = __builtin_fmaf(p, __builtin_amdgcn_rcpf(counted[j][i]) * (1.0f / kSumUnit), l[rb]);
                     w[4 * j + i] = T(p);
+                    rest[4 * j + i] = T(p - float(w[4 * j + i]));
                 }
             __builtin_memcpy(&p8[rb], w, 16);
+            __builtin_memcpy(&rest8[rb], rest, 16);
         }
 #pragma unroll
         for (int c = 0; c < C; c++)
@@ -405,7 +415,10 @@ __global__ __launch_bounds__(256) void k_attn_rows(AttnArgs a) {
                 const x8 v = codes8<T>(vc[0][c][k], vc[1][c][k]);
 #pragma unroll
                 for (int rb = 0; rb < RT; rb++)
-                    if (rb == 0 || two) o[rb][c][k] = Half<T>::mfma16(v, p8[rb], o[rb][c][k]);
+                    if (rb == 0 || two) {
+                        o[rb][c][k] = Half<T>::mfma16(v, p8[rb], o[rb][c][k]);
+                        o[rb][c][k] = Half<T>::mfma16(v, rest8[rb], o[rb][c][k]);
+                    }
             }
     }
 
@@ -561,6 +574,7 @@ __global__ __launch_bounds__(64 * WAVES) void k_attn_tile(AttnArgs a) {
     constexpr int LOADS = 8 * D / THREADS;               // 16-byte loads of a lane for 64 keys and 64 values
     constexpr float NEG = -__builtin_inff();
     static_assert(8 * D % (2 * THREADS) == 0, "whole loads of keys and of values");
+    constexpr bool REST = sizeof(O) == 4;                 // fp32 outputs: a second product of what the weights' rounding leaves
     constexpr int RING = D == 256 ? 2 : 3;                // buffers of 64 keys, and of 64 values
     __shared__ __align__(16) uint8_t S_k[RING][128 * D], S_v[RING][128 * D];
     __shared__ __align__(16) float S_ks[4][64], S_lv[4][64], S_rv[4][64];
@@ -583,7 +597,8 @@ __global__ __launch_bounds__(64 * WAVES) void k_attn_tile(AttnArgs a) {
     // this lane's row
     const int r = row0 + 32 * wv + col, tok = r / a.G;
     const bool there = r < rows;
-    const int pos = there ? s.pos0 + tok : -1, first = a.window ? pos - a.window : -1;
+    const int pos = there ? s.pos0 + tok : -1;
+    const uint32_t span = a.window ? uint32_t(a.window) : 0x80000000u;      // keys that a row sees, up to its position
     // A lane past the last row has zeros: any row that it could read instead is one that, with the output over the
     // queries, another workgroup may be writing.
     x8 q[KS];
@@ -742,7 +757,7 @@ __global__ __launch_bounds__(64 * WAVES) void k_attn_tile(AttnArgs a) {
 #pragma unroll
                 for (int e = 0; e < 32; e++) {
                     const int key = key0 + 8 * (e / 4) + 4 * hf + e % 4;
-                    if (!((there4 >> (e / 8) & 1) && key <= pos && key > first)) sc[e / 16][e % 16] = NEG;
+                    if (!((there4 >> (e / 8) & 1) && uint32_t(pos - key) < span)) sc[e / 16][e % 16] = NEG;
                     top = fmaxf(top, sc[e / 16][e % 16]);
                 }
                 top = max_of_halves(top);
@@ -759,7 +774,7 @@ __global__ __launch_bounds__(64 * WAVES) void k_attn_tile(AttnArgs a) {
                     for (int i = 0; i < 16; i++) o[d][i] *= f;
             }
             const float ref = m == NEG ? 0.0f : m;
-            union { T w[32]; x8 p[4]; } u;
+            union { T w[32]; x8 p[4]; } u, rest;
             float pair = 0.0f;
             f32x16 nx[2];
             f32x4 k4[2], v4[2];
@@ -780,6 +795,10 @@ __global__ __launch_bounds__(64 * WAVES) void k_attn_tile(AttnArgs a) {
                     if (e & 1) {
                         u.w[e - 1] = T(pair);
                         u.w[e] = T(p);
+                        if constexpr (REST) {
+                            rest.w[e - 1] = T(pair - float(u.w[e - 1]));
+                            rest.w[e] = T(p - float(u.w[e]));
+                        }
                     }
                     pair = p;
                 }
@@ -798,6 +817,7 @@ __global__ __launch_bounds__(64 * WAVES) void k_attn_tile(AttnArgs a) {
             for (int g = 0; g < N; g++) {
                 if (WAVES == 8 && g == 0) __builtin_amdgcn_s_setprio(0);
                 o[g % DT] = Half<T>::mfma32(fr[g % AHEAD], u.p[g / DT], o[g % DT]);
+                if constexpr (REST) o[g % DT] = Half<T>::mfma32(fr[g % AHEAD], rest.p[g / DT], o[g % DT]);
                 if (g + AHEAD < N)
                     fr[g % AHEAD] = *reinterpret_cast<const x8 *>(V + (g + AHEAD) * 1024);
                 else if (RING > 2)

@@ -9,7 +9,7 @@ h half a step of q's type, N keys, s a value's scale, t scores in units of log2:
     2^121, whose terms are subnormal.  Counted twice, for the weights and for
     their sum, which is scaled in two halves where a reference moves and where
     shares meet, 6u each time, counted as 100 u;
-  - w s rounds to 16 bits: h of itself, or in fp16 2^-31 of the row's largest at
+  - w s rounds to 16 bits: h of itself (h^2 where it is held in two parts), or in fp16 2^-31 of the row's largest at
     worst, times codes of 127 and N: N 2^-24 of the largest product;
   - a scale counts as 2^-100, or 2^-108 of the largest of its sequence, at least,
     so values are off by 127 times that (zeros are not, their codes are 0);
@@ -26,9 +26,9 @@ from tests.test_gpu_attention import BF16, DEV, F16, F32, U, Batch, gen, heads, 
 pytestmark = pytest.mark.gpu
 
 
-def check(bt, out, window=0, every=1):
+def check(bt, out, window=0, every=1, parts=1):
     (kc, kd), (vc, vd) = kvcache.unpack(bt.cache, bt.D)
-    h16, i, scale = torch.finfo(bt.q.dtype).eps / 2, 0, bt.D ** -0.5 * math.log2(math.e)
+    h16, i, scale = (torch.finfo(bt.q.dtype).eps / 2) ** parts, 0, bt.D ** -0.5 * math.log2(math.e)
     for b, (n, N) in enumerate(zip(bt.new, bt.lens_h)):
         slot = bt.slots[b].to(DEV)
         pos, key = torch.arange(N - n, N, device=DEV)[:, None], torch.arange(N, device=DEV)[None]
