@@ -510,9 +510,9 @@ int mmq_kv_read(int type, const void *cache, int64_t n_pages, int page, int head
  *   its first max_q computed.
  * Rounding: q and the codes enter the products as they are, sums are fp32;
  * exp(..) times a value's scale enters the second product as two numbers of q's
- * type (16 bits for bf16, 22 for fp16), or, where out is not fp32 and a sequence
- * may have more than 32 rows (max_q tokens of q_heads / kv_heads heads), as one;
- * the output is rounded once to its own type.  A value's scale below 2^-100, or
+ * type (16 bits for bf16, 22 for fp16); as one, it may be, where out is not fp32
+ * and a sequence may have more than 32 rows (max_q times q_heads / kv_heads).
+ * The output is rounded once to its own type.  A value's scale below 2^-100, or
  * below 2^-108 of the largest of its sequence, may count as that.  Where a
  * key's weight times its value's scale (as it counts) is below 2^-118 of its
  * row's largest such product, its part of the output may be lost, and below
