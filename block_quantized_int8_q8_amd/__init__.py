@@ -670,7 +670,7 @@ def rope_frequencies(rot, base=10000.0, scaling=None, factor=1.0, low=1.0, high=
         raise ValueError(f"unknown scaling {scaling!r}: expected one of {list(ROPE_SCALINGS)}")
     if high is None:
         high = 32.0 if scaling == "yarn" else 4.0
-    freqs, mscale = torch.empty(max(int(rot) // 2, 1), dtype=torch.float64), ctypes.c_double()
+    freqs, mscale = torch.empty(max(int(rot) // 2, 1), dtype=torch.float64, device="cpu"), ctypes.c_double()
     _check(lib().mmq_rope_frequencies(ROPE_SCALINGS[scaling], rot, base, factor, low, high,
                                       0 if original is None else original, ctypes.c_void_p(freqs.data_ptr()),
                                       ctypes.byref(mscale)), "mmq_rope_frequencies")
