@@ -49,8 +49,10 @@ inline const char *check_strides(int64_t ldt, int64_t ldh) {
 // ... of one that is written: no element may have two places in it.
 inline const char *check_out_strides(int64_t T, int64_t H, int64_t D, int64_t ldt, int64_t ldh) {
     if (const char *bad = check_strides(ldt, ldh)) return bad;
+    if (T == 0) return nullptr;
     const bool heads_inside = (H == 1 || ldh >= D) && (T == 1 || ldt >= (H - 1) * ldh + D);
-    const bool tokens_inside = (T == 1 || ldt >= D) && (H == 1 || ldh >= (T - 1) * ldt + D);
+    // ldh >= (T - 1) * ldt + D, of which the product may pass 64 bits
+    const bool tokens_inside = (T == 1 || ldt >= D) && (H == 1 || (ldh >= D && (T == 1 || ldt <= (ldh - D) / (T - 1))));
     if (!heads_inside && !tokens_inside) return "the output's tokens or heads overlap";
     return nullptr;
 }
