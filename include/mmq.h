@@ -525,8 +525,10 @@ int mmq_kv_read(int type, const void *cache, int64_t n_pages, int page, int head
  * every sequence, and past max_q, are left as they were.  Lengths are clamped to
  * 0..max_pages*page and offsets to 0..T; where offsets decrease, rows between
  * them are unspecified, but nothing outside the buffers is read or written.
- * T * q_heads <= 2^30; n_seqs <= 2^20; max_pages * page <= 2^30; a grid of
- * more than 2^22 workgroups (n_seqs * kv_heads and more) is refused.
+ * T * q_heads <= 2^30; n_seqs <= 2^20; max_pages * page <= 2^30.  A call that
+ * needs too many workgroups for one launch is refused: 2^23 (n_seqs * kv_heads)
+ * where sequences may have 32 rows or fewer, 2^22 (kv_heads for every 128 rows,
+ * 256 with D = 128, and for the end of every sequence) where they may have more.
  * The same bits on every run; which shares a sequence's keys are split into
  * (and so the last bits) depends on the whole batch's lengths.
  * workspace: mmq_attention_workspace_bytes for the same sizes (0: may be NULL),
