@@ -121,6 +121,7 @@ inline const char *check_rope(int D, int rot, int layout) {
 constexpr int kAttnFewRows = 32;          // most rows of a sequence in the rows kernel
 constexpr int kAttnRowsChunk = 128;       // keys: least share of a workgroup of the rows kernel
 constexpr int kAttnTileChunk = 256;       // ... of the tile kernel
+constexpr int kAttnAlongKeys = 8192;      // keys from which the tile kernel takes no few-row sequence along
 
 struct AttnPlan {
     int few_tiles;            // rows kernel: 16-row blocks per workgroup (1, 2); 0: not launched
@@ -163,10 +164,17 @@ inline bool make_plan_attention(int64_t T, int64_t B, int Hq, int Hkv, int D, in
     // Where sequences have many rows on the average, the tile kernel takes the
     // few-row ones along: they run beside its tiles, the rows kernel would
     // run before them (24 sequences, half of them decoding, half chunks of up
-    // to 700 tokens: 160 -> 145 us; one prompt: a launch less).
+    // to 700 tokens: 160 -> 145 us; one prompt: a launch less).  Not where one
+    // of them may hold many keys, which the tile kernel does not split once its
+    // tiles fill the device, 2 us for 64 keys: along and apart, a prompt of 2048
+    // tokens and one decoded token over 4096 keys 83 and 93 us, over 8192 107 and
+    // 89, over 256K 2640 and 176; a prompt of 8192 and seven over 256K 5350 and
+    // 920; 24 mixed ones of up to 8192 keys 403 and 419.  (What a table could hold
+    // decides, as lengths are on the device: one with room for more than its
+    // sequences have pays the second launch, about 10 us, for nothing.)
     // And where T says that all have max_q, none has few (16 sequences of 40
     // rows over 8192 keys 75 -> 71 us).
-    if (most_rows <= kAttnFewRows || (G <= kAttnFewRows && T * G < 128 * B && T < B * max_q)) {
+    if (most_rows <= kAttnFewRows || (G <= kAttnFewRows && T < B * max_q && (T * G < 128 * B || max_keys >= kAttnAlongKeys))) {
         p->few_tiles = (most_rows < kAttnFewRows ? most_rows : kAttnFewRows) > 16 ? 2 : 1;
         const int64_t units = B * Hkv;
         int64_t s = ceil_div(4 * int64_t(p->few_target), units);        // lengths differ: more shares than the device needs

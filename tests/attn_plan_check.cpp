@@ -52,6 +52,8 @@ int main() {
         CHECK(p.few_tiles || p.tile_rows);
         CHECK(p.few_bytes >= 0 && p.few_bytes % 256 == 0 && p.tile_bytes >= 0 && p.tile_bytes % 256 == 0);
         const int64_t few = p.few_tiles ? kAttnFewRows : 0;
+        // a few-row sequence of many keys has the kernel that splits them, unless T says that there is none
+        if (G <= kAttnFewRows && T < B * std::min(max_q, T) && max_pages * page >= 8192) CHECK(p.few_tiles);
         if (!p.tile_rows) CHECK(longest * G <= 16 * p.few_tiles);        // all rows have a place in the rows kernel
         if (p.few_tiles) {
             CHECK(p.few_grid == B * Hkv * p.few_split && p.few_grid * 256 < (int64_t(1) << 32));
