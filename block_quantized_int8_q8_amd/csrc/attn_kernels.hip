@@ -57,7 +57,7 @@ struct AttnArgs {
     void *out;                // [T, Hq, D]
     int64_t odt, odh;
     int64_t n_pages, max_pages;
-    int page_shift, Hq, Hkv, G;
+    int page_shift, Hkv, G;
     int T, B, max_q, window;
     float scale;              // softmax scale times log2(e)
     float *part;              // shares: outputs, then (reference, sum) pairs
@@ -905,12 +905,12 @@ __global__ __launch_bounds__(64 * WAVES) void k_attn_tile(AttnArgs a) {
 struct Joined {
     f32x4 v;
     float sum;
-    // One share, for the largest reference `to` of all: one that saw no
-    // finite maximum adds nothing, unless it holds a NaN.
+    // One share, for the largest reference `to` of all, finite: one that saw
+    // no finite maximum adds nothing, unless it holds a NaN.
     __device__ __forceinline__ void add(float m, float l, f32x4 o, float to) {
-        const bool none = m == -__builtin_inff();
-        sum += none ? l : scaled_sum(l, m - to);
-        v += o * (none ? 0.0f : __builtin_amdgcn_exp2f(m - to));
+        const float h = __builtin_amdgcn_exp2f(0.5f * (m - to));
+        sum += l * h * h;                                 // in two halves, as in scaled_sum
+        v += o * (h * h);
     }
     template <typename O>
     __device__ __forceinline__ void write(const AttnArgs &a, const Seq &s, int h, int r, int d) const {
@@ -927,7 +927,6 @@ struct Joined {
 template <typename O, int D, int R>
 __global__ __launch_bounds__(256) void k_attn_join_rows(AttnArgs a, int most_rows) {
     constexpr int LANES = D / 4, GROUPS = 256 / LANES, EARLY = 4;
-    constexpr float NEG = -__builtin_inff();
     __shared__ float S_v[GROUPS][D], S_l[GROUPS];
     const int r = blockIdx.x % most_rows, unit = blockIdx.x / most_rows, h = unit % a.Hkv, b = unit / a.Hkv;
     const int group = threadIdx.x / LANES, d = 4 * (threadIdx.x % LANES);
@@ -946,7 +945,7 @@ __global__ __launch_bounds__(256) void k_attn_join_rows(AttnArgs a, int most_row
     if (s.n == 0 || !has_few_rows(a, s.n) || r >= s.n * a.G) return;          // no share was written
     const int shares = reinterpret_cast<const int *>(ml + 2 * slots)[unit];
     if (shares <= 1) return;
-    float to = NEG;
+    float to = -__FLT_MAX__;
     for (int k = threadIdx.x & 63; k < shares; k += 64) to = fmaxf(to, ml[2 * (slot0 + int64_t(k) * R)]);
 #pragma unroll
     for (int o = 32; o; o >>= 1) to = fmaxf(to, __shfl_xor(to, o));
@@ -988,7 +987,7 @@ __global__ __launch_bounds__(256) void k_attn_join_tiles(AttnArgs a) {
     if (shares <= 1 || r >= rows) return;
     const int64_t slot0 = int64_t(unit) * a.split * BM + slot_r;
     const float *ml = a.part + int64_t(a.units) * a.Hkv * a.split * BM * D;
-    float to = -__builtin_inff();
+    float to = -__FLT_MAX__;
 #pragma unroll 8
     for (int k = 0; k < shares; k++) to = fmaxf(to, ml[2 * (slot0 + int64_t(k) * BM)]);
     Joined j{{0, 0, 0, 0}, 0.0f};
@@ -1054,7 +1053,7 @@ hipError_t launch_attention(const AttnPlan &p, int type, const void *q, int64_t 
     a.out = out; a.odt = odt; a.odh = odh;
     a.n_pages = n_pages; a.max_pages = max_pages;
     a.page_shift = __builtin_ctz(unsigned(page));
-    a.Hq = Hq; a.Hkv = Hkv; a.G = Hq / Hkv;
+    a.Hkv = Hkv; a.G = Hq / Hkv;
     a.T = int(T); a.B = int(B); a.max_q = int(max_q < T ? max_q : T); a.window = window;
     a.scale = float(double(scale) * 1.4426950408889634074);
     a.few_rows = p.few_tiles ? kAttnFewRows : 0;

@@ -284,7 +284,7 @@ __global__ __launch_bounds__(256) void k_kv_write(const TI *__restrict__ k, int6
     }
 }
 
-// Sixteen tokens of up to four heads a workgroup.  Codes pass through LDS so
+// Sixteen tokens of kWriteHeads heads a workgroup.  Codes pass through LDS so
 // that what is neighbours in the cache is written together: a key's 16 bytes
 // beside the next tokens', a value's four tokens as one dword (written a byte
 // at a time, 32768 tokens of 4 heads of 128 took 60 us; so 24).
