@@ -396,15 +396,17 @@ __global__ __launch_bounds__(256) void k_attn_rows(AttnArgs a) {
             }
             const float ref = m[rb] == NEG ? 0.0f : m[rb];
             T w[8], rest[8];
+            float sum = 0.0f;                                        // of eight: below 2^117
 #pragma unroll
             for (int j = 0; j < 2; j++)
 #pragma unroll
                 for (int i = 0; i < 4; i++) {
                     const float p = __builtin_amdgcn_exp2f(t[j][i] - ref);
-                    l[rb] = __builtin_fmaf(p, __builtin_amdgcn_rcpf(counted[j][i]) * (1.0f / kSumUnit), l[rb]);
+                    sum = __builtin_fmaf(p, __builtin_amdgcn_rcpf(counted[j][i]), sum);
                     w[4 * j + i] = T(p);
                     rest[4 * j + i] = T(p - float(w[4 * j + i]));
                 }
+            l[rb] = __builtin_fmaf(sum, 1.0f / kSumUnit, l[rb]);
             __builtin_memcpy(&p8[rb], w, 16);
             __builtin_memcpy(&rest8[rb], rest, 16);
         }
