@@ -242,10 +242,15 @@ __device__ __forceinline__ float max_of_halves(float x) {
 // matrix instruction's fragments, 1 KiB a load, no LDS and no wait for
 // another wave before the end.  Rows are the other operand, 16 or 32 of them,
 // so that a group of query heads reads its keys once.
-//   64 sequences of 2K to 16K keys, 28 on 4 heads of 128: 101 us for 506 MB =
-//   5.0 TB/s (a copy moves 5.12), and 6.6 for the join of its shares
-//   one sequence of 256K keys, 32 on 4 heads: 60 us for 277 MB, join 8
-//   one of 2011 keys: 5.9 us, a chain of offsets, pages, keys; join 3.8
+//   64 sequences of 2K to 16K keys, 28 on 4 heads of 128: 104 us for 506 MB =
+//   4.9 TB/s (a copy moves 5.12), and 6.5 for the join of its shares
+//   one sequence of 256K keys, 32 on 4 heads: 61 us for 277 MB, join 8
+//   one of 2011 keys: 7.3 us, a chain of offsets, pages, keys; join 3.6
+// Heads of 64 have half the bytes for the same softmax, about 260 vector
+// instructions for 32 keys: 64 sequences of 8192 keys 61 us in bf16 and 57 in
+// fp16 (53 and 54 with weights of one part, and the sum not held apart from the
+// values' sizes) against 56 for the bytes; heads of 128 106 (106), of 256 211
+// (216).
 template <typename T, typename O, int D, int RT>
 __global__ __launch_bounds__(256) void k_attn_rows(AttnArgs a) {
     typedef typename Half<T>::x8 x8;
@@ -491,11 +496,13 @@ __global__ __launch_bounds__(256) void k_attn_rows(AttnArgs a) {
 // and lie in LDS in the order of the matrix instruction's fragments: every
 // read is 1 KiB in a row.
 //
-// What bounds it (8192 x 8192 causal, 28 on 4 heads of 128, bf16: 514 us = 936
-// TFLOP/s; a large library product reaches 1233): VALU and matrix core
-// together.  A step of a wave is 32 products of 32 cycles and about 260 other
-// vector instructions, 32 of them exponentials and 48 conversions; a product costs the VALU two to three instructions' time.  The matrix cores
-// are busy 41 % of the time at 1.9 GHz, where the power limit holds the clock.
+// What bounds it (8192 x 8192 causal, 28 on 4 heads of 128, bf16: 512 to 527 us
+// from day to day, 913 to 939 TFLOP/s; a large library product reaches 1233):
+// VALU and matrix core together.  A step of a wave is 32 products of 32 cycles
+// and 221 other vector instructions, 32 of them exponentials and 48 conversions;
+// a product costs the VALU two to three instructions' time.  In a run of 600 us
+// at 1.9 GHz, where the power limit holds the clock, the matrix cores are busy
+// 42 % of the time.
 // Steps that led here, us: scores, softmax and output one after the other
 // 677; next scores behind this step's exponentials, scales behind the
 // output's products, values' scales in the exponent 543; three buffers,

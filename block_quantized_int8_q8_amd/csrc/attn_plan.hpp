@@ -116,8 +116,8 @@ inline const char *check_rope(int D, int rot, int layout) {
 // sequence of few rows runs in the rows kernel, of more in the tile kernel.
 // Both kernels decide from the sequence's own row count on the device, so a
 // batch may mix them.  Where the border lies: 16 sequences of 8192 keys, 32 on
-// 4 heads of 128, 8, 16 and 32 rows each in the rows kernel 30, 32 and 49 us;
-// 40, 64 and 128 rows in the tile kernel 71, 70 and 76.
+// 4 heads of 128, 8, 16 and 32 rows each in the rows kernel 32, 33 and 51 us;
+// 40, 64 and 128 rows in the tile kernel 71, 72 and 78.
 constexpr int kAttnFewRows = 32;          // most rows of a sequence in the rows kernel
 constexpr int kAttnRowsChunk = 128;       // keys: least share of a workgroup of the rows kernel
 constexpr int kAttnTileChunk = 256;       // ... of the tile kernel
@@ -154,10 +154,14 @@ inline bool make_plan_attention(int64_t T, int64_t B, int Hq, int Hkv, int D, in
     const int64_t G = Hq / Hkv, max_keys = max_pages * page;
     if (max_q > T) max_q = T;
     const int64_t most_rows = max_q * G;
-    // Three workgroups of the rows kernel a CU: four are resident, and the
-    // shares' remainders take the fourth's place (64 sequences of 2K to 16K
-    // keys, kernel and join together: target of 2 per CU 122 us, 3 112, 4 129,
-    // 6 118; one of 256K keys 59, 61, 64, 67).
+    // Three workgroups of the rows kernel a CU: four of one row block with heads
+    // of 64 and 128 are resident (128 registers), and the shares' remainders
+    // take the fourth's place (64 sequences of 2K to 16K keys, kernel and join
+    // together: target of 2 per CU 122 us, 3 112, 4 129, 6 118; one of 256K keys
+    // 59, 61, 64, 67).  Of two row blocks with heads of 64 three are resident,
+    // with heads of 128 two, of heads of 256 two and one: there the same target
+    // runs its shares in rounds (64 sequences of 8192 keys with heads of 256 211
+    // us, 213 by the bytes).
     p->few_target = 3 * cu_count;
     p->tile_target = D == 64 ? 2 * cu_count : cu_count;
     auto ceil_div = [](int64_t a, int64_t b) { return (a + b - 1) / b; };
