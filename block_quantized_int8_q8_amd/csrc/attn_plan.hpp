@@ -177,7 +177,8 @@ inline bool make_plan_attention(int64_t T, int64_t B, int Hq, int Hkv, int D, in
     // decides, as lengths are on the device: one with room for more than its
     // sequences have pays the second launch, about 10 us, for nothing.)
     // And where T says that all have max_q, none has few (16 sequences of 40
-    // rows over 8192 keys 75 -> 71 us).
+    // rows over 8192 keys 75 -> 71 us); a batch padded to B max_q rows says so
+    // too, and has its short sequences in the tile kernel.
     if (most_rows <= kAttnFewRows || (G <= kAttnFewRows && T < B * max_q && (T * G < 128 * B || max_keys >= kAttnAlongKeys))) {
         p->few_tiles = (most_rows < kAttnFewRows ? most_rows : kAttnFewRows) > 16 ? 2 : 1;
         const int64_t units = B * Hkv;

@@ -489,8 +489,9 @@ int mmq_kv_write(int type, const void *k, int64_t k_ldt, int64_t k_ldh, const vo
                  int64_t T, void *cache, int64_t n_pages, int page, int heads, int D, void *stream);
 
 /* The values that slots hold: code times scale in fp32, rounded to `type`.
- *   k, v: [T, heads, D] of `type`; slots: int32 [T], in any order, repeats
- *   allowed.  Rows of a slot outside the cache are left as they were. */
+ *   k, v: [T, heads, D] of `type`, not overlapping each other or the cache;
+ *   slots: int32 [T], in any order, repeats allowed.  Rows of a slot outside
+ *   the cache are left as they were. */
 int mmq_kv_read(int type, const void *cache, int64_t n_pages, int page, int heads, int D, const int32_t *slots, int64_t T,
                 void *k, int64_t k_ldt, int64_t k_ldh, void *v, int64_t v_ldt, int64_t v_ldh, void *stream);
 
