@@ -496,8 +496,8 @@ __global__ __launch_bounds__(256) void k_attn_rows(AttnArgs a) {
 // and lie in LDS in the order of the matrix instruction's fragments: every
 // read is 1 KiB in a row.
 //
-// What bounds it (8192 x 8192 causal, 28 on 4 heads of 128, bf16: 512 to 527 us
-// from day to day, 913 to 939 TFLOP/s; a large library product reaches 1233):
+// What bounds it (8192 x 8192 causal, 28 on 4 heads of 128, bf16: 512 to 547 us
+// from card to card, 880 to 939 TFLOP/s; a large library product reaches 1233):
 // VALU and matrix core together.  A step of a wave is 32 products of 32 cycles
 // and 221 other vector instructions, 32 of them exponentials and 48 conversions;
 // a product costs the VALU two to three instructions' time.  In a run of 600 us
